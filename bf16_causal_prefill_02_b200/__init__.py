@@ -11,7 +11,9 @@ Low-level names mirror the C ABI (``zq_attn_fwd``, ``zq_attn_fwd_ex``,
 a stream handle).  The torch-level helpers ``attn_fwd``, ``quantize_fp8``,
 ``quantize_fp8_multi``, ``quantize_fp8_grouped`` and ``flash_attn_func``
 marshal tensors into those calls; ``attn_plan``
-returns the schedule of a call (host only).
+returns the schedule of a call (host only).  ``kv_append`` and ``attn_decode``
+carry on where the prompt ends: new keys and values into a paged cache, and
+attention of one new token over it.
 """
 from __future__ import annotations
 
@@ -66,6 +68,18 @@ class zq_attn_plan(ctypes.Structure):
     ]
 
 
+class zq_paged_kv(ctypes.Structure):
+    _fields_ = [
+        ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+        ("k_page_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+        ("block_table", ctypes.c_void_p), ("cache_seqlens", ctypes.c_void_p),
+        ("k_descale", ctypes.c_void_p), ("v_descale", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("table_width", ctypes.c_int), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("B", ctypes.c_int),
+        ("Hkv", ctypes.c_int), ("d_qk", ctypes.c_int), ("d_v", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("descale_per_head", ctypes.c_int),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -98,6 +112,12 @@ def _load():
     lib.zq_quantize_grouped_workspace_bytes.restype = ctypes.c_size_t
     lib.zq_quantize_noalloc_scratch_bytes.argtypes = []
     lib.zq_quantize_noalloc_scratch_bytes.restype = ctypes.c_size_t
+    lib.zq_kv_append.argtypes = [ctypes.POINTER(zq_paged_kv), P, P, i64, i64, P, i64, P]
+    lib.zq_kv_append.restype = i32
+    lib.zq_attn_decode.argtypes = [ctypes.POINTER(zq_paged_kv), P, i64, i32, f32, P, P, P, P]
+    lib.zq_attn_decode.restype = i32
+    lib.zq_decode_workspace_bytes.argtypes = []
+    lib.zq_decode_workspace_bytes.restype = ctypes.c_size_t
     lib.zq_debug_exp2.argtypes = [P, P, i64, i32, P]
     lib.zq_debug_exp2.restype = i32
     lib.zq_quantize_workspace_bytes.argtypes = []
@@ -199,6 +219,18 @@ def zq_quantize_grouped_workspace_bytes(B, H, heads_per_scale) -> int:
 
 def zq_quantize_noalloc_scratch_bytes() -> int:
     return int(_lib.zq_quantize_noalloc_scratch_bytes())
+
+
+def zq_kv_append(cache: zq_paged_kv, k, v, k_stride, v_stride, cu_seqlens, T, stream) -> int:
+    return _lib.zq_kv_append(ctypes.byref(cache), k, v, k_stride, v_stride, cu_seqlens, T, stream)
+
+
+def zq_attn_decode(cache: zq_paged_kv, q, q_stride, Hq, softmax_scale, out, lse, workspace, stream) -> int:
+    return _lib.zq_attn_decode(ctypes.byref(cache), q, q_stride, Hq, softmax_scale, out, lse, workspace, stream)
+
+
+def zq_decode_workspace_bytes() -> int:
+    return int(_lib.zq_decode_workspace_bytes())
 
 
 def zq_debug_exp2(x, y, n, degree, stream) -> int:
@@ -489,6 +521,149 @@ def flash_attn_func(q, k, v, softmax_scale=None, causal=True, return_attn_probs=
     out, lse = attn_fwd(q, k, v, softmax_scale=softmax_scale, causal=causal,
                         return_lse=return_attn_probs, **fp8_kwargs)
     return (out, lse, None) if return_attn_probs else out
+
+
+def _on(device, stream, call):
+    """call(raw stream handle) with `device` current and, where `stream` (a
+    torch stream or a raw handle) is given, with that stream current, so that
+    what the call allocates belongs to the stream that uses it."""
+    cuda = _torch().cuda
+    if stream is None:
+        if cuda.current_device() == device:
+            return call(cuda.current_stream().cuda_stream)
+        with cuda.device(device):
+            return call(cuda.current_stream().cuda_stream)
+    if not hasattr(stream, "cuda_stream"):
+        stream = cuda.ExternalStream(int(stream), device=device) if int(stream) else cuda.default_stream(device)
+    elif stream.device.index != device:
+        raise ValueError("stream is on %s, expected cuda:%d" % (stream.device, device))
+    with cuda.stream(stream):
+        return call(stream.cuda_stream)
+
+
+def _check_on(device, **tensors):
+    """Every given tensor lives on CUDA device `device` (an index; -1: the host, which is refused)."""
+    for name, t in tensors.items():
+        if t is not None and (t.get_device() != device or device < 0):
+            if not t.is_cuda:
+                raise ValueError("%s must be a CUDA tensor" % name)
+            raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, device))
+
+
+def _row_stride(name, t):
+    """The stride of t's first dimension (0: contiguous); the others must be
+    contiguous, and the rows must not overlap."""
+    if t.is_contiguous():
+        return 0
+    row, stride = t.numel() // max(t.shape[0], 1), t.stride(0)
+    if t.shape[0] > 1 and stride < row or not t[0].is_contiguous():
+        raise ValueError("%s must be contiguous in all but its first dimension, its rows apart" % name)
+    return stride if t.shape[0] > 1 else 0
+
+
+def _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale):
+    """The zq_paged_kv of these tensors."""
+    torch = _torch()
+    if k_cache.dim() != 4 or v_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be 4-D (pages, page size, kv heads, dim)")
+    if k_cache.dtype == v_cache.dtype == torch.bfloat16:
+        dtype = ZQ_DTYPE_BF16
+    elif _is_fp8(k_cache) and _is_fp8(v_cache):
+        dtype = ZQ_DTYPE_FP8_E4M3
+    else:
+        raise TypeError("k_cache and v_cache must both be bfloat16 or both FP8 e4m3")
+    pages, page_size, Hkv, dqk = k_cache.shape
+    dv = v_cache.shape[3]
+    if v_cache.shape[:3] != k_cache.shape[:3]:
+        raise ValueError("v_cache must have k_cache's pages, page size and heads %s, got %s"
+                         % (tuple(k_cache.shape[:3]), tuple(v_cache.shape[:3])))
+    if block_table.dim() != 2 or block_table.dtype != torch.int32:
+        raise ValueError("block_table must be a 2-D int32 tensor (batch, pages per sequence)")
+    B, width = block_table.shape
+    if cache_seqlens.dtype != torch.int32 or tuple(cache_seqlens.shape) != (B,) or not cache_seqlens.is_contiguous():
+        raise ValueError("cache_seqlens must be a contiguous int32 tensor of %d lengths" % B)
+    per_head = 0
+    if dtype == ZQ_DTYPE_FP8_E4M3:
+        for name, t in (("k_descale", k_descale), ("v_descale", v_descale)):
+            if t is not None and (t.dtype != torch.float32 or not t.is_contiguous()):
+                raise ValueError("%s must be a contiguous float32 tensor" % name)
+        per_head = _descale_layout(1, Hkv, k_descale, v_descale)
+    else:
+        k_descale = v_descale = None
+    ks, vs, ts = _row_stride("k_cache", k_cache), _row_stride("v_cache", v_cache), _row_stride("block_table", block_table)
+    _check_on(k_cache.get_device(), k_cache=k_cache, v_cache=v_cache, block_table=block_table, cache_seqlens=cache_seqlens,
+              k_descale=k_descale, v_descale=v_descale)
+    return zq_paged_kv(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, block_table.data_ptr(), cache_seqlens.data_ptr(),
+                       _ptr(k_descale), _ptr(v_descale), ts, width, pages, page_size, B, Hkv, dqk, dv, dtype, per_head)
+
+
+def kv_append(k, v, k_cache, v_cache, block_table, cache_seqlens, cu_seqlens=None, k_descale=None, v_descale=None, stream=None):
+    """New keys and values into a paged cache, as zq_kv_append.
+
+    k (T,Hkv,d_qk), v (T,Hkv,d_v) bfloat16, packed over the sequences that
+    cu_seqlens (int32, B + 1) delimits; without it one token per sequence
+    (T == B).  Rows may be strided (views into a fused projection).
+    k_cache (pages, page size, Hkv, d_qk), v_cache (pages, page size, Hkv, d_v)
+    bfloat16, or FP8 e4m3 with fp32 descales (one value, or one per kv head):
+    written in place.  Sequence b's tokens go to positions cache_seqlens[b]
+    onwards of the pages in block_table[b]; cache_seqlens is not advanced.
+    Returns (k_cache, v_cache)."""
+    torch = _torch()
+    c = _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale)
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+        raise TypeError("k and v must be bfloat16")
+    if k.dim() != 3 or tuple(k.shape[1:]) != (c.Hkv, c.d_qk):
+        raise ValueError("k must have shape (tokens, %d, %d), got %s" % (c.Hkv, c.d_qk, tuple(k.shape)))
+    T = k.shape[0]
+    if tuple(v.shape) != (T, c.Hkv, c.d_v):
+        raise ValueError("v must have shape %s, got %s" % ((T, c.Hkv, c.d_v), tuple(v.shape)))
+    if cu_seqlens is None:
+        if T != c.B:
+            raise ValueError("without cu_seqlens there is one token for each of the %d sequences, got %d" % (c.B, T))
+    elif cu_seqlens.dtype != torch.int32 or tuple(cu_seqlens.shape) != (c.B + 1,) or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous int32 tensor of %d offsets" % (c.B + 1))
+    device = k_cache.get_device()
+    _check_on(device, k=k, v=v, cu_seqlens=cu_seqlens)
+    ks, vs = _row_stride("k", k), _row_stride("v", v)
+    _on(device, stream, lambda s: _check(zq_kv_append(c, k.data_ptr(), v.data_ptr(), ks, vs, _ptr(cu_seqlens), T, s),
+                                         "zq_kv_append"))
+    return k_cache, v_cache
+
+
+def attn_decode(q, k_cache, v_cache, block_table, cache_seqlens, out=None, lse=None, softmax_scale=None, k_descale=None,
+                v_descale=None, workspace=None, return_lse=True, stream=None):
+    """Attention of one new token per sequence over a paged cache, as zq_attn_decode.
+
+    q (B,Hq,d_qk) bfloat16 (rows may be strided); the cache as for kv_append,
+    with cache_seqlens (int32, B) keys in each sequence.
+    Returns (out bf16 (B,Hq,d_v), lse fp32 (B,Hq) or None)."""
+    torch = _torch()
+    c = _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale)
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16")
+    if q.dim() != 3 or q.shape[0] != c.B or q.shape[2] != c.d_qk:
+        raise ValueError("q must have shape (%d, heads, %d), got %s" % (c.B, c.d_qk, tuple(q.shape)))
+    B, Hq = q.shape[0], q.shape[1]
+    if out is not None:
+        _check_buffer("out", out, (B, Hq, c.d_v), torch.bfloat16)
+    if lse is not None:
+        _check_buffer("lse", lse, (B, Hq), torch.float32)
+    nbytes = zq_decode_workspace_bytes()
+    if workspace is not None and (workspace.numel() * workspace.element_size() < nbytes or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous and hold zq_decode_workspace_bytes() bytes")
+    device = k_cache.get_device()
+    _check_on(device, q=q, out=out, lse=lse, workspace=workspace)
+    qs = _row_stride("q", q)
+
+    def call(s):
+        o = torch.empty((B, Hq, c.d_v), dtype=torch.bfloat16, device=q.device) if out is None else out
+        e = torch.empty((B, Hq), dtype=torch.float32, device=q.device) if lse is None and return_lse else lse
+        w = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if workspace is None else workspace
+        _check(zq_attn_decode(c, q.data_ptr(), qs, Hq, float(softmax_scale) if softmax_scale else 0.0, o.data_ptr(), _ptr(e),
+                              w.data_ptr(), s), "zq_attn_decode")
+        return o, e
+
+    return _on(device, stream, call)
 
 
 def causal_flops(B, Sq, Hq, dqk, dv, Sk=None) -> float:

@@ -1,0 +1,109 @@
+// kv_append.cu -- new keys and values into a paged cache, as they are (bf16)
+// or rounded to e4m3 with the cache's scales.
+//
+// One warp per token: it finds the token's sequence (a 32-ary search of the
+// sequence offsets), looks up the page its position falls in, and moves the
+// token's key and value rows, 16 bytes a lane at a time.  Bound by memory:
+// 2 bytes read and 2 (bf16) or 1 (e4m3) written per element.
+#include "paged.cuh"
+
+namespace zq {
+
+namespace {
+
+constexpr int kAppendWarps = 8;
+
+// The sequence whose tokens [cu[b], cu[b + 1]) hold t: the number of offsets
+// cu[0..B] that are <= t, minus 1 (B or -1: no sequence holds it).  All lanes
+// of the warp take part.
+__device__ __forceinline__ int find_sequence(const int32_t* __restrict__ cu, int B, int64_t t, int lane) {
+  int lo = 0, n = B + 1;  // offsets lo .. lo + n - 1 are undecided; those before lo are <= t
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int at = lo + min((lane + 1) * step, n) - 1;  // the last offset of this lane's piece
+    const bool mine = lane * step < n;
+    const unsigned le = __ballot_sync(0xffffffffu, mine && cu[at] <= t);
+    const int full = __popc(le);  // pieces that lie wholly at or below t (offsets ascend)
+    lo += min(full * step, n);
+    n = min(step, n - min(full * step, n));
+    if (step == 1) break;
+    n = max(n - 1, 0);  // the last offset of the piece is above t
+  }
+  return lo - 1;
+}
+
+// 16 bytes (8 bf16) to 8 e4m3 codes: rne_satfinite(fl32(x * inv)).
+__device__ __forceinline__ uint2 to_e4m3(uint4 x, float inv) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16) * inv;
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * inv;
+  }
+  return make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
+}
+
+// A scale of 0 stands for a head whose values were all 0: its codes are 0.
+__device__ __forceinline__ float inverse_scale(const float* ds, int per_head, int h) {
+  const float s = ds ? ds[per_head ? h : 0] : 1.0f;
+  return s == 0.0f ? 0.0f : __frcp_rn(s);
+}
+
+template <int FP8>
+__global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const AppendLaunch a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const PagedKV& c = a.c;
+  int b = (int)t, i = 0;
+  if (a.cu) {
+    b = find_sequence(a.cu, c.B, t, lane);
+    if (b < 0 || b >= c.B) return;  // not a token of any sequence
+    i = (int)(t - a.cu[b]);
+  }
+  const int have = c.seqlens[b];
+  const int64_t pos = (int64_t)have + i;
+  const int64_t page_at = pos >> c.page_shift;
+  if (have < 0 || page_at >= c.table_width) return;  // no room: the token is dropped
+  const int page = c.table[b * c.table_stride + page_at];
+  if (page < 0 || page >= c.num_pages) return;
+  const int64_t row = pos & ((1 << c.page_shift) - 1);
+  const int es = FP8 ? 1 : 2;
+  const int nk = c.Hkv * c.dqk / 8, nv = c.Hkv * c.dv / 8;  // pieces of 8 elements
+  char* dk = c.k + page * c.k_page + row * c.Hkv * c.dqk * es;
+  char* dv = c.v + page * c.v_page + row * c.Hkv * c.dv * es;
+  const uint4* sk = reinterpret_cast<const uint4*>(a.k + t * a.k_stride);
+  const uint4* sv = reinterpret_cast<const uint4*>(a.v + t * a.v_stride);
+#pragma unroll 4
+  for (int x = lane; x < nk; x += 32) {
+    const uint4 w = __ldg(sk + x);
+    if (FP8)
+      reinterpret_cast<uint2*>(dk)[x] = to_e4m3(w, inverse_scale(c.k_descale, c.descale_per_head, x * 8 / c.dqk));
+    else
+      reinterpret_cast<uint4*>(dk)[x] = w;
+  }
+#pragma unroll 4
+  for (int x = lane; x < nv; x += 32) {
+    const uint4 w = __ldg(sv + x);
+    if (FP8)
+      reinterpret_cast<uint2*>(dv)[x] = to_e4m3(w, inverse_scale(c.v_descale, c.descale_per_head, x * 8 / c.dv));
+    else
+      reinterpret_cast<uint4*>(dv)[x] = w;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const AppendLaunch& a, cudaStream_t st) {
+  if (a.T <= 0) return cudaSuccess;
+  const int64_t blocks = (a.T + kAppendWarps - 1) / kAppendWarps;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (a.c.dtype == 1)
+    kv_append_kernel<1><<<(unsigned)blocks, kAppendWarps * 32, 0, st>>>(a);
+  else
+    kv_append_kernel<0><<<(unsigned)blocks, kAppendWarps * 32, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace zq

@@ -345,6 +345,95 @@ int zq_quantize_fp8_grouped(const void* x, int x_dtype, int B, int64_t S, int H,
   return e == cudaSuccess ? ZQ_OK : ZQ_ERR_CUDA;
 }
 
+// The cache as the kernels address it, after validation.
+static int paged_cache(const zq_paged_kv* a, zq::PagedKV* c) {
+  if (!a) return ZQ_ERR_NULL;
+  if (!a->k_cache || !a->v_cache || !a->block_table || !a->cache_seqlens) return ZQ_ERR_NULL;
+  if (a->B <= 0 || a->Hkv <= 0 || a->num_pages <= 0 || a->table_width <= 0) return ZQ_ERR_SHAPE;
+  if (a->page_size <= 0 || a->page_size > 65536 || (a->page_size & (a->page_size - 1)) != 0) return ZQ_ERR_SHAPE;
+  if (!((a->d_qk == 128 && a->d_v == 128) || (a->d_qk == 192 && a->d_v == 128))) return ZQ_ERR_UNSUPPORTED;
+  if (a->dtype != ZQ_DTYPE_BF16 && a->dtype != ZQ_DTYPE_FP8_E4M3) return ZQ_ERR_UNSUPPORTED;
+  if (a->descale_per_head != 0 && a->descale_per_head != 1) return ZQ_ERR_UNSUPPORTED;
+  if ((int64_t)a->table_width * a->page_size > ((int64_t)1 << 30) || a->Hkv > 4096 || a->B > 65535) return ZQ_ERR_SHAPE;
+  if (a->table_stride != 0 && (a->table_stride < a->table_width || a->table_stride > ((int64_t)1 << 40))) return ZQ_ERR_SHAPE;
+  const int es = a->dtype == ZQ_DTYPE_BF16 ? 2 : 1;
+  const int64_t kp = (int64_t)a->page_size * a->Hkv * a->d_qk, vp = (int64_t)a->page_size * a->Hkv * a->d_v;
+  const int64_t ks = a->k_page_stride ? a->k_page_stride : kp, vs = a->v_page_stride ? a->v_page_stride : vp;
+  if (ks < kp || vs < vp || ks > ((int64_t)1 << 40) || vs > ((int64_t)1 << 40)) return ZQ_ERR_SHAPE;
+  if (!aligned16(a->k_cache) || !aligned16(a->v_cache) || (ks * es) % 16 != 0 || (vs * es) % 16 != 0) return ZQ_ERR_ALIGN;
+  c->k = static_cast<char*>(a->k_cache);
+  c->v = static_cast<char*>(a->v_cache);
+  c->k_page = ks * es;
+  c->v_page = vs * es;
+  c->table = a->block_table;
+  c->seqlens = a->cache_seqlens;
+  c->k_descale = a->dtype == ZQ_DTYPE_FP8_E4M3 ? a->k_descale : nullptr;
+  c->v_descale = a->dtype == ZQ_DTYPE_FP8_E4M3 ? a->v_descale : nullptr;
+  c->table_stride = a->table_stride ? a->table_stride : a->table_width;
+  c->descale_per_head = a->descale_per_head;
+  c->B = a->B;
+  c->Hkv = a->Hkv;
+  c->num_pages = a->num_pages;
+  c->page_shift = 0;
+  while ((1 << c->page_shift) < a->page_size) ++c->page_shift;
+  c->table_width = a->table_width;
+  c->dqk = a->d_qk;
+  c->dv = a->d_v;
+  c->dtype = a->dtype;
+  return ZQ_OK;
+}
+
+int zq_kv_append(const zq_paged_kv* cache, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                 const int32_t* cu_seqlens, int64_t T, void* stream) {
+  zq::AppendLaunch L;
+  int rc = paged_cache(cache, &L.c);
+  if (rc != ZQ_OK) return rc;
+  if (T < 0 || T > 0x7fffffffLL || (!cu_seqlens && T != cache->B)) return ZQ_ERR_SHAPE;
+  if (T > 0 && (!k || !v)) return ZQ_ERR_NULL;
+  const int64_t kr = (int64_t)cache->Hkv * cache->d_qk, vr = (int64_t)cache->Hkv * cache->d_v;
+  const int64_t ks = k_stride ? k_stride : kr, vs = v_stride ? v_stride : vr;
+  if (ks < kr || vs < vr || ks > ((int64_t)1 << 31) || vs > ((int64_t)1 << 31)) return ZQ_ERR_SHAPE;
+  if (!aligned16(k) || !aligned16(v) || ks % 8 != 0 || vs % 8 != 0) return ZQ_ERR_ALIGN;
+  rc = check_device(nullptr);
+  if (rc != ZQ_OK) return rc;
+  L.k = static_cast<const char*>(k);
+  L.v = static_cast<const char*>(v);
+  L.k_stride = ks * 2;
+  L.v_stride = vs * 2;
+  L.cu = cu_seqlens;
+  L.T = T;
+  cudaError_t e = zq::launch_kv_append(L, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ZQ_OK : ZQ_ERR_CUDA;
+}
+
+size_t zq_decode_workspace_bytes(void) { return zq::decode_workspace_bytes(); }
+
+int zq_attn_decode(const zq_paged_kv* cache, const void* q, int64_t q_stride, int Hq, float softmax_scale,
+                   void* out, float* lse, void* workspace, void* stream) {
+  zq::DecodeLaunch L;
+  int rc = paged_cache(cache, &L.c);
+  if (rc != ZQ_OK) return rc;
+  if (!q || !out || !workspace) return ZQ_ERR_NULL;
+  if (Hq <= 0 || Hq > 4096 || Hq % cache->Hkv != 0) return ZQ_ERR_SHAPE;
+  if (!std::isfinite(softmax_scale)) return ZQ_ERR_SHAPE;
+  const int64_t qr = (int64_t)Hq * cache->d_qk, qs = q_stride ? q_stride : qr;
+  if (qs < qr || qs > ((int64_t)1 << 31)) return ZQ_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || (lse && !aligned16(lse)) || qs % 8 != 0)
+    return ZQ_ERR_ALIGN;
+  int sms = 0;
+  rc = check_device(&sms);
+  if (rc != ZQ_OK) return rc;
+  L.q = q;
+  L.q_stride = qs;
+  L.Hq = Hq;
+  L.softmax_scale = softmax_scale > 0.0f ? softmax_scale : (float)(1.0 / std::sqrt((double)cache->d_qk));
+  L.out = out;
+  L.lse = lse;
+  L.workspace = workspace;
+  cudaError_t e = zq::launch_decode(L, static_cast<cudaStream_t>(stream), sms);
+  return e == cudaSuccess ? ZQ_OK : ZQ_ERR_CUDA;
+}
+
 int zq_debug_exp2(const float* x, float* y, int64_t n, int degree, void* stream) {
   if (n < 0) return ZQ_ERR_SHAPE;
   if (n > 0 && (!x || !y)) return ZQ_ERR_NULL;

@@ -86,6 +86,44 @@ struct QuantItems {
 };
 cudaError_t launch_quantize_multi(QuantItems Q, int count, void* workspace, cudaStream_t st, int num_sms);
 void* noalloc_scratch_for_device(int dev);
+
+// A paged cache as the kernels address it: key c of sequence b is row
+// c & (page_size - 1) of page block_table[b * table_stride + (c >> page_shift)].
+// Strides in bytes.
+struct PagedKV {
+  char* k;
+  char* v;
+  int64_t k_page, v_page;
+  const int32_t* table;
+  const int32_t* seqlens;
+  const float* k_descale;  // 1 or Hkv fp32, or nullptr (1.0)
+  const float* v_descale;
+  int64_t table_stride;
+  int descale_per_head;
+  int B, Hkv, num_pages, page_shift, table_width;
+  int dqk, dv, dtype;
+};
+struct AppendLaunch {
+  PagedKV c;
+  const char* k;
+  const char* v;
+  int64_t k_stride, v_stride;  // bytes between tokens
+  const int32_t* cu;           // B + 1 token offsets, or nullptr (token t is sequence t's)
+  int64_t T;
+};
+cudaError_t launch_kv_append(const AppendLaunch& a, cudaStream_t st);
+struct DecodeLaunch {
+  PagedKV c;
+  const void* q;
+  int64_t q_stride;  // elements between sequences
+  int Hq;
+  float softmax_scale;
+  void* out;
+  float* lse;
+  void* workspace;
+};
+cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t st, int num_sms);
+size_t decode_workspace_bytes();
 cudaError_t launch_exp2_check(const float* x, float* y, int64_t n, int degree, cudaStream_t st);
 size_t noalloc_scratch_capacity();
 

@@ -342,6 +342,100 @@ ZQ_API int zq_quantize_fp8_grouped(const void* x, int x_dtype, int B, int64_t S,
  * (4 per slot, rounded up to 16); 0 for arguments it would reject. */
 ZQ_API size_t zq_quantize_grouped_workspace_bytes(int B, int H, int heads_per_scale);
 
+/*
+ * A paged key-value cache.  Pages hold page_size keys of every kv head; key c
+ * of sequence b is row c % page_size of page block_table[b * table_stride +
+ * c / page_size].  (The pages that this library follows cover prefill only;
+ * these operators carry a prompt's result on to the tokens that come after.)
+ *
+ *   k_cache  (num_pages, page_size, Hkv, d_qk), the last three contiguous,
+ *            bf16 (ZQ_DTYPE_BF16) or e4m3 bytes (ZQ_DTYPE_FP8_E4M3)
+ *   v_cache  (num_pages, page_size, Hkv, d_v), same type
+ *   k_page_stride, v_page_stride  elements from one page to the next; 0 means
+ *            page_size * Hkv * d (contiguous).  At least that, and a
+ *            multiple of 16 bytes.  Keys and values may interleave in one
+ *            allocation.
+ *   block_table  (B, >= table_width) int32, table_stride entries from one
+ *            sequence to the next (0 means table_width)
+ *   cache_seqlens  B int32: keys the cache holds for each sequence.  A value
+ *            below 0 counts as 0, one above table_width * page_size as that.
+ *   page_size a power of two up to 65536; (d_qk, d_v) in {(128,128), (192,128)};
+ *   table_width * page_size at most 2^30, B at most 65535, heads at most 4096.
+ *   k_descale, v_descale: e4m3 only.  The value of a code is code * descale.
+ *            One fp32, or Hkv fp32 with descale_per_head = 1; NULL means 1.0.
+ * Entries of the table outside [0, num_pages) are never followed: a key on
+ * such a page is treated as not there.
+ */
+typedef struct zq_paged_kv {
+  void* k_cache;
+  void* v_cache;
+  int64_t k_page_stride, v_page_stride;
+  const int32_t* block_table;
+  const int32_t* cache_seqlens;
+  const float* k_descale;
+  const float* v_descale;
+  int64_t table_stride;
+  int table_width;
+  int num_pages, page_size;
+  int B, Hkv, d_qk, d_v;
+  int dtype;
+  int descale_per_head;
+} zq_paged_kv;
+
+/*
+ * zq_kv_append -- writes new keys and values into the cache.
+ *
+ *   k  (T, Hkv, d_qk) bf16, v (T, Hkv, d_v) bf16: the tokens of all
+ *      sequences, packed; the last two dimensions contiguous, k_stride /
+ *      v_stride elements from one token to the next (0: contiguous;
+ *      multiples of 8).
+ *   cu_seqlens  B + 1 int32, ascending: tokens cu_seqlens[b] ..
+ *      cu_seqlens[b + 1] - 1 are sequence b's.  NULL: one token for each
+ *      sequence (T must equal B).
+ *   Token t of sequence b goes to position cache_seqlens[b] + t -
+ *   cu_seqlens[b].  bf16 caches take the bits as they are; e4m3 caches
+ *   e4m3_rne_satfinite(fl32(x * fl32(1 / descale))), and code 0 where the
+ *   descale is 0 and x is finite.
+ * cache_seqlens is read, not advanced.  Tokens of no sequence, and tokens
+ * whose position lies past the table or on a page outside [0, num_pages), are
+ * dropped.  Two tokens that the table sends to the same place are the
+ * caller's error: that place then holds parts of either.
+ * T == 0 does nothing (k, v may then be NULL).
+ * Errors: ZQ_ERR_NULL, ZQ_ERR_SHAPE (sizes <= 0, T < 0 or != B without
+ *   cu_seqlens, a stride too small, page_size no power of two, products past
+ *   the limits above), ZQ_ERR_UNSUPPORTED (head dims, dtype, descale_per_head
+ *   not 0 or 1), ZQ_ERR_ALIGN (k, v, caches or strides not multiples of 16
+ *   bytes), ZQ_ERR_ARCH, ZQ_ERR_CUDA.
+ */
+ZQ_API int zq_kv_append(const zq_paged_kv* cache, const void* k, const void* v, int64_t k_stride,
+                        int64_t v_stride, const int32_t* cu_seqlens, int64_t T, void* stream);
+
+/*
+ * zq_attn_decode -- attention of one new token per sequence over the cache,
+ *   out = softmax(q k^T * softmax_scale) v over the cache_seqlens[b] keys of
+ *   sequence b (the new token's own key among them, once it is appended).
+ *
+ *   q    (B, Hq, d_qk) bf16, the last two dimensions contiguous, q_stride
+ *        elements from one sequence to the next (0: contiguous; a multiple
+ *        of 8).  Hq % Hkv == 0; head h reads kv head h / (Hq / Hkv).
+ *   out  (B, Hq, d_v) contiguous bf16;  lse (B, Hq) fp32 natural log, or NULL.
+ *   softmax_scale <= 0 selects 1/sqrt(d_qk).
+ *   workspace  device scratch of zq_decode_workspace_bytes() bytes, 16-byte
+ *        aligned; its contents on entry do not matter and it must not be
+ *        used by another call that runs at the same time.
+ * A sequence without keys (length 0, or no key on a page of the cache) gets
+ * out = 0, lse = -inf.  Rows past a sequence's length are not read.  e4m3
+ * codes enter the products exactly (as f16); the weights are rounded to bf16
+ * (bf16 caches) or f16 (e4m3 caches), sums are fp32.
+ * Two stream operations (two kernels).  Runs repeat bit for bit.
+ * Errors: as zq_kv_append, with q, out, lse and workspace.
+ */
+ZQ_API int zq_attn_decode(const zq_paged_kv* cache, const void* q, int64_t q_stride, int Hq,
+                          float softmax_scale, void* out, float* lse, void* workspace, void* stream);
+
+/* Bytes of device scratch zq_attn_decode needs (a constant, about 9 MB). */
+ZQ_API size_t zq_decode_workspace_bytes(void);
+
 /* zq_debug_exp2 -- y[i] = 2^x[i] by the kernels' software exp2 (degree 3 or
  * 4 minimax polynomial after range reduction), by CUDA's exp2f (degree 0) or
  * by the hardware approximation ex2.approx (degree -1).  x, y: device fp32
