@@ -11,8 +11,9 @@ Low-level names mirror the C ABI (``zq_attn_fwd``, ``zq_attn_fwd_ex``,
 a stream handle).  The torch-level helpers ``attn_fwd``, ``quantize_fp8``,
 ``quantize_fp8_multi``, ``quantize_fp8_grouped`` and ``flash_attn_func``
 marshal tensors into those calls; ``attn_plan``
-returns the schedule of a call (host only).  ``kv_append`` and ``attn_decode``
-carry on where the prompt ends: new keys and values into a paged cache, and
+returns the schedule of a call (host only).  ``attn_varlen`` and
+``flash_attn_varlen_func`` take packed prompts of different lengths;
+``kv_append`` and ``attn_decode`` carry on where the prompt ends: new keys and values into a paged cache, and
 attention of one new token over it.
 """
 from __future__ import annotations
@@ -68,6 +69,20 @@ class zq_attn_plan(ctypes.Structure):
     ]
 
 
+class zq_varlen_args(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("cu_seqlens_q", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("total_q", ctypes.c_int), ("total_k", ctypes.c_int), ("Hq", ctypes.c_int),
+        ("Hkv", ctypes.c_int), ("d_qk", ctypes.c_int), ("d_v", ctypes.c_int),
+        ("softmax_scale", ctypes.c_float), ("causal", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("q_descale", ctypes.c_void_p), ("k_descale", ctypes.c_void_p), ("v_descale", ctypes.c_void_p),
+        ("softmax_mode", ctypes.c_int), ("block_scale", ctypes.c_int), ("headroom_T", ctypes.c_int),
+        ("status", ctypes.c_void_p), ("descale_layout", ctypes.c_int),
+    ]
+
+
 class zq_paged_kv(ctypes.Structure):
     _fields_ = [
         ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
@@ -112,6 +127,8 @@ def _load():
     lib.zq_quantize_grouped_workspace_bytes.restype = ctypes.c_size_t
     lib.zq_quantize_noalloc_scratch_bytes.argtypes = []
     lib.zq_quantize_noalloc_scratch_bytes.restype = ctypes.c_size_t
+    lib.zq_attn_varlen_fwd.argtypes = [ctypes.POINTER(zq_varlen_args), P]
+    lib.zq_attn_varlen_fwd.restype = i32
     lib.zq_kv_append.argtypes = [ctypes.POINTER(zq_paged_kv), P, P, i64, i64, P, i64, P]
     lib.zq_kv_append.restype = i32
     lib.zq_attn_decode.argtypes = [ctypes.POINTER(zq_paged_kv), P, i64, i32, f32, P, P, P, P]
@@ -219,6 +236,10 @@ def zq_quantize_grouped_workspace_bytes(B, H, heads_per_scale) -> int:
 
 def zq_quantize_noalloc_scratch_bytes() -> int:
     return int(_lib.zq_quantize_noalloc_scratch_bytes())
+
+
+def zq_attn_varlen_fwd(args: zq_varlen_args, stream) -> int:
+    return _lib.zq_attn_varlen_fwd(ctypes.byref(args), stream)
 
 
 def zq_kv_append(cache: zq_paged_kv, k, v, k_stride, v_stride, cu_seqlens, T, stream) -> int:
@@ -559,6 +580,82 @@ def _row_stride(name, t):
     if t.shape[0] > 1 and stride < row or not t[0].is_contiguous():
         raise ValueError("%s must be contiguous in all but its first dimension, its rows apart" % name)
     return stride if t.shape[0] > 1 else 0
+
+
+def attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, out=None, lse=None, softmax_scale=None, causal=True, q_descale=None,
+                k_descale=None, v_descale=None, softmax_mode=ZQ_SOFTMAX_LEANP, block_scale=True, headroom_T=8, status=None,
+                return_lse=True, stream=None):
+    """Causal prefill attention over packed prompts, as zq_attn_varlen_fwd.
+
+    q (total_q,Hq,d_qk), k (total_k,Hkv,d_qk), v (total_k,Hkv,d_v): bfloat16,
+    or FP8 e4m3 with fp32 descales (one value each, or B * Hkv values, one per
+    sequence and kv head).  cu_seqlens_q, cu_seqlens_k: int32 CUDA tensors of
+    B + 1 ascending row offsets.
+    Returns (out bf16 (total_q,Hq,d_v), lse fp32 (Hq,total_q) or None); rows
+    of no sequence are not written."""
+    torch = _torch()
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dim() != 3:
+            raise ValueError("%s must be 3-D (rows, heads, dim), got %d-D" % (name, t.dim()))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+    if q.dtype == k.dtype == v.dtype == torch.bfloat16:
+        dtype = ZQ_DTYPE_BF16
+    elif _is_fp8(q) and _is_fp8(k) and _is_fp8(v):
+        dtype = ZQ_DTYPE_FP8_E4M3
+    else:
+        raise TypeError("q, k, v must all be bfloat16 or all FP8 e4m3")
+    Tq, Hq, dqk = q.shape
+    Tk, Hkv, _ = k.shape
+    dv = v.shape[2]
+    if k.shape[2] != dqk:
+        raise ValueError("k must have q's head dim %d, got %d" % (dqk, k.shape[2]))
+    if v.shape[0] != Tk or v.shape[1] != Hkv:
+        raise ValueError("v must have k's rows and head count (%d, %d), got (%d, %d)" % (Tk, Hkv, v.shape[0], v.shape[1]))
+    n = cu_seqlens_q.numel()
+    for name, t in (("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_k", cu_seqlens_k)):
+        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or n < 2 or t.numel() != n:
+            raise ValueError("%s must be a contiguous 1-D int32 tensor of B + 1 offsets, as long as the other" % name)
+    B = n - 1
+    if out is not None:
+        _check_buffer("out", out, (Tq, Hq, dv), torch.bfloat16)
+    if lse is not None:
+        _check_buffer("lse", lse, (Hq, Tq), torch.float32)
+    layout = ZQ_DESCALE_PER_TENSOR
+    if dtype == ZQ_DTYPE_FP8_E4M3:
+        for name, t in (("q_descale", q_descale), ("k_descale", k_descale), ("v_descale", v_descale)):
+            if t is not None and (t.dtype != torch.float32 or not t.is_contiguous()):
+                raise ValueError("%s must be a contiguous float32 tensor" % name)
+        layout = _descale_layout(B, Hkv, q_descale, k_descale, v_descale)
+    else:
+        q_descale = k_descale = v_descale = None
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status must be an int32 tensor with at least one element")
+    device = q.get_device()
+    _check_on(device, q=q, k=k, v=v, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, out=out, lse=lse, q_descale=q_descale,
+              k_descale=k_descale, v_descale=v_descale, status=status)
+
+    def call(s):
+        o = torch.empty((Tq, Hq, dv), dtype=torch.bfloat16, device=q.device) if out is None else out
+        e = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device) if lse is None and return_lse else lse
+        a = zq_varlen_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(e), cu_seqlens_q.data_ptr(),
+                           cu_seqlens_k.data_ptr(), B, Tq, Tk, Hq, Hkv, dqk, dv, float(softmax_scale) if softmax_scale else 0.0,
+                           int(bool(causal)), dtype, _ptr(q_descale), _ptr(k_descale), _ptr(v_descale), int(softmax_mode),
+                           int(bool(block_scale)), int(headroom_T), _ptr(status), layout)
+        _check(zq_attn_varlen_fwd(a, s), "zq_attn_varlen_fwd")
+        return o, e
+
+    return _on(device, stream, call)
+
+
+def flash_attn_varlen_func(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=None, max_seqlen_k=None, softmax_scale=None,
+                           causal=True, return_attn_probs=False, **fp8_kwargs):
+    """flash_attn_varlen_func-style entry over attn_varlen.  The longest
+    lengths are accepted and not needed.  With return_attn_probs=True returns
+    (out, lse, None)."""
+    out, lse = attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, softmax_scale=softmax_scale, causal=causal,
+                           return_lse=return_attn_probs, **fp8_kwargs)
+    return (out, lse, None) if return_attn_probs else out
 
 
 def _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale):

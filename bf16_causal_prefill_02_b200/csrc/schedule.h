@@ -115,6 +115,20 @@ inline int choose_head_group(int B, int Hq, int Hkv, int Sq, int Sk, int d_qk, i
   return bh;
 }
 
+// Packed prompts: heads whose units are interleaved.  All of them while the K
+// and V of all heads stay in L2 (the 96 MB of choose_head_group), else the
+// query heads of as few kv heads as make at least 4.
+inline int choose_varlen_head_group(int Hq, int Hkv, int64_t Tk, int d_qk, int d_v, int elem_bytes) {
+  if ((double)Hkv * Tk * (d_qk + d_v) * elem_bytes <= 96.0 * 1024 * 1024) return Hq;
+  const int group = Hq / Hkv;
+  int kv = 1;
+  while (kv * group < 4 && kv < Hkv) {
+    do ++kv;
+    while (Hkv % kv != 0);
+  }
+  return kv * group;
+}
+
 // Short sequences (at most 64 query tiles) run persistent: one CTA per SM,
 // each walking its share of the units, so that a unit's loads and first QK
 // overlap the previous unit's tail.  Longer ones launch a CTA per unit: the

@@ -36,11 +36,10 @@ int check_device(int* num_sms) {
   return ZQ_OK;
 }
 
-int validate_attn(const zq_attn_args* a) {
-  if (!a) return ZQ_ERR_NULL;
-  if (!a->q || !a->k || !a->v || !a->out) return ZQ_ERR_NULL;
-  if (a->B <= 0 || a->Sq <= 0 || a->Sk <= 0 || a->Hq <= 0 || a->Hkv <= 0) return ZQ_ERR_SHAPE;
-  if (a->Hq % a->Hkv != 0) return ZQ_ERR_SHAPE;
+// Head dims, element type, FP8 options and scale, which zq_attn_args and
+// zq_varlen_args name alike.
+template <class Args>
+int validate_options(const Args* a) {
   if (!((a->d_qk == 128 && a->d_v == 128) || (a->d_qk == 192 && a->d_v == 128)))
     return ZQ_ERR_UNSUPPORTED;
   if (a->dtype != ZQ_DTYPE_BF16 && a->dtype != ZQ_DTYPE_FP8_E4M3) return ZQ_ERR_UNSUPPORTED;
@@ -53,6 +52,16 @@ int validate_attn(const zq_attn_args* a) {
       return ZQ_ERR_UNSUPPORTED;
   }
   if (!(std::isfinite(a->softmax_scale))) return ZQ_ERR_SHAPE;
+  return ZQ_OK;
+}
+
+int validate_attn(const zq_attn_args* a) {
+  if (!a) return ZQ_ERR_NULL;
+  if (!a->q || !a->k || !a->v || !a->out) return ZQ_ERR_NULL;
+  if (a->B <= 0 || a->Sq <= 0 || a->Sk <= 0 || a->Hq <= 0 || a->Hkv <= 0) return ZQ_ERR_SHAPE;
+  if (a->Hq % a->Hkv != 0) return ZQ_ERR_SHAPE;
+  const int rc = validate_options(a);
+  if (rc != ZQ_OK) return rc;
   // units = n_qtiles * B * Hq stay in int range, with room above the last
   // unit for the persistent CTAs' zigzag walk (it computes indices up to
   // two rounds of CTAs past the last unit); TMA element counts and strides
@@ -342,6 +351,57 @@ int zq_quantize_fp8_grouped(const void* x, int x_dtype, int B, int64_t S, int H,
       x, x_dtype == ZQ_X_BF16, B, S, H, d, heads_per_scale,
       hadamard ? (d % 128 == 0 ? 1 : 2) : 0, x_fp8, descale, workspace,
       static_cast<cudaStream_t>(stream), sms);
+  return e == cudaSuccess ? ZQ_OK : ZQ_ERR_CUDA;
+}
+
+int zq_attn_varlen_fwd(const zq_varlen_args* a, void* stream) {
+  if (!a) return ZQ_ERR_NULL;
+  if (!a->cu_seqlens_q || !a->cu_seqlens_k) return ZQ_ERR_NULL;
+  if (a->B <= 0 || a->B > 65535 || a->total_q < 0 || a->total_k < 0 || a->Hq <= 0 || a->Hkv <= 0 || a->Hq > 4096)
+    return ZQ_ERR_SHAPE;
+  if ((a->total_q > 0 && (!a->q || !a->out)) || (a->total_k > 0 && (!a->k || !a->v))) return ZQ_ERR_NULL;
+  if (a->Hq % a->Hkv != 0) return ZQ_ERR_SHAPE;
+  int rc = validate_options(a);
+  if (rc != ZQ_OK) return rc;
+  // the grid (a bound on the query tiles, times Hq) stays in 31 bits
+  const int64_t max_tiles = a->total_q > 0 ? (a->total_q + 127 * (int64_t)a->B) / 128 : 0;
+  if (max_tiles * a->Hq > 0x7FFF0000ll) return ZQ_ERR_SHAPE;
+  if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->out) || !aligned16(a->lse)) return ZQ_ERR_ALIGN;
+  rc = check_device(nullptr);
+  if (rc != ZQ_OK) return rc;
+  zq::VarlenLaunch L;
+  L.q = a->q;
+  // without any key the tensor maps of k and v are never loaded from
+  L.k = a->total_k > 0 ? a->k : a->q;
+  L.v = a->total_k > 0 ? a->v : a->q;
+  L.dqk = a->d_qk;
+  L.dtype = a->dtype;
+  L.mode = a->softmax_mode;
+  L.block_scale = a->block_scale;
+  const bool fp8 = a->dtype == ZQ_DTYPE_FP8_E4M3;
+  zq::VarlenParams& p = L.p;
+  p.out = a->out;
+  p.lse = a->lse;
+  p.cu_q = a->cu_seqlens_q;
+  p.cu_k = a->cu_seqlens_k;
+  p.q_descale = a->q_descale;
+  p.k_descale = a->k_descale;
+  p.v_descale = a->v_descale;
+  p.status = a->status;
+  p.descale_per_kv = fp8 && a->descale_layout == ZQ_DESCALE_PER_KV_HEAD ? 1 : 0;
+  p.B = a->B;
+  p.Tq = a->total_q;
+  p.Tk = a->total_k;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.group = a->Hq / a->Hkv;
+  p.max_tiles = (int)max_tiles;
+  p.head_group = zq::choose_varlen_head_group(a->Hq, a->Hkv, a->total_k, a->d_qk, a->d_v, fp8 ? 1 : 2);
+  p.causal = a->causal ? 1 : 0;
+  p.headroom_T = fp8 ? a->headroom_T : 8;
+  p.softmax_scale = a->softmax_scale > 0.0f ? a->softmax_scale : (float)(1.0 / std::sqrt((double)a->d_qk));
+  p.timeout_ns = kTimeoutNs;
+  cudaError_t e = zq::launch_attention_varlen(L, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ZQ_OK : ZQ_ERR_CUDA;
 }
 

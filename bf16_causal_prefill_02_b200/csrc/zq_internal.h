@@ -87,6 +87,34 @@ struct QuantItems {
 cudaError_t launch_quantize_multi(QuantItems Q, int count, void* workspace, cudaStream_t st, int num_sms);
 void* noalloc_scratch_for_device(int dev);
 
+// Attention over packed prompts.
+struct VarlenParams {
+  void* out;   // (Tq, Hq, d_v) bfloat16
+  float* lse;  // (Hq, Tq) or nullptr
+  const int32_t* cu_q;  // B + 1 row offsets
+  const int32_t* cu_k;
+  const float* q_descale;
+  const float* k_descale;
+  const float* v_descale;
+  int* status;
+  int descale_per_kv;  // entry b * Hkv + kv head, as in AttnParams
+  int B, Tq, Tk, Hq, Hkv, group;
+  int max_tiles;   // bound on the 128-row query tiles of all sequences
+  int head_group;  // query heads whose units are interleaved; divides Hq
+  int causal;
+  int headroom_T;
+  float softmax_scale;
+  uint64_t timeout_ns;
+};
+struct VarlenLaunch {
+  const void* q;
+  const void* k;
+  const void* v;
+  VarlenParams p;
+  int dqk, dtype, mode, block_scale;
+};
+cudaError_t launch_attention_varlen(const VarlenLaunch& a, cudaStream_t st);
+
 // A paged cache as the kernels address it: key c of sequence b is row
 // c & (page_size - 1) of page block_table[b * table_stride + (c >> page_shift)].
 // Strides in bytes.

@@ -343,6 +343,57 @@ ZQ_API int zq_quantize_fp8_grouped(const void* x, int x_dtype, int B, int64_t S,
 ZQ_API size_t zq_quantize_grouped_workspace_bytes(int B, int H, int heads_per_scale);
 
 /*
+ * zq_attn_varlen_fwd -- zq_attn_fwd over packed prompts of different lengths.
+ * [P3 TL;DR: causal forward (prefill) attention; the packed form is the one a
+ *  server's prompt batch comes in.]
+ *
+ *   q    (total_q, Hq,  d_qk) contiguous, bf16 or e4m3 bytes
+ *   k    (total_k, Hkv, d_qk), v (total_k, Hkv, d_v) contiguous, same type
+ *   cu_seqlens_q, cu_seqlens_k  B + 1 int32 each, on the device, ascending:
+ *        sequence b has query rows cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1
+ *        and key rows cu_seqlens_k[b] .. cu_seqlens_k[b + 1] - 1.  Offsets
+ *        outside the tensors are clamped to them; a sequence whose offsets
+ *        descend has no rows (its neighbours' rows are then undefined, but
+ *        nothing outside the tensors is read or written).
+ *   out  (total_q, Hq, d_v) contiguous bf16;  lse (Hq, total_q) fp32 or NULL.
+ *        Rows of no sequence (before the first offset, behind the last) are
+ *        left as they were.
+ *   causal: bottom-right per sequence, key c visible to query i iff
+ *        c <= i + Sk_b - Sq_b; a query row with no visible key gets out = 0,
+ *        lse = -inf.  Sq_b and Sk_b may be 0.
+ *   descale_layout ZQ_DESCALE_PER_KV_HEAD: entry b * Hkv + kv head.
+ *   The other fields as in zq_attn_args.
+ * Keys and values must be finite within a sequence (a weight of 0 times an
+ * infinity is NaN); what other rows hold does not matter.
+ * total_q == 0 does nothing; total_k == 0 gives 0 and -inf (k, v may be NULL).
+ * One kernel launch, no workspace.  Errors: as zq_attn_fwd_ex; ZQ_ERR_SHAPE
+ * also for B > 65535, Hq > 4096 and (total_q / 128 + B) * Hq past 31 bits.
+ */
+typedef struct zq_varlen_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;
+  const int32_t* cu_seqlens_q;
+  const int32_t* cu_seqlens_k;
+  int B, total_q, total_k, Hq, Hkv, d_qk, d_v;
+  float softmax_scale;
+  int causal;
+  int dtype;
+  const float* q_descale;
+  const float* k_descale;
+  const float* v_descale;
+  int softmax_mode;
+  int block_scale;
+  int headroom_T;
+  int* status;
+  int descale_layout;
+} zq_varlen_args;
+
+ZQ_API int zq_attn_varlen_fwd(const zq_varlen_args* args, void* stream);
+
+/*
  * A paged key-value cache.  Pages hold page_size keys of every kv head; key c
  * of sequence b is row c % page_size of page block_table[b * table_stride +
  * c / page_size].  (The pages that this library follows cover prefill only;

@@ -139,3 +139,81 @@ def test_descales_of_a_cache():
         zq.attn_decode(_t(2, 4, 128), **c, k_descale=torch.ones(2), v_descale=torch.ones(1))
     with pytest.raises(ValueError, match="descales must all hold"):
         zq.kv_append(_t(2, 2, 128), _t(2, 2, 128), **c, k_descale=torch.ones(3))
+
+
+# ------------------------------------------------------------ packed prompts
+def _varlen(**kw):
+    a = zq.zq_varlen_args()
+    d = dict(q=A, k=A, v=A, out=A, lse=None, cu_seqlens_q=A, cu_seqlens_k=A, B=2, total_q=300, total_k=300, Hq=4, Hkv=2, d_qk=128, d_v=128,
+             softmax_scale=0.0, causal=1, dtype=0, q_descale=None, k_descale=None, v_descale=None, softmax_mode=zq.ZQ_SOFTMAX_LEANP,
+             block_scale=1, headroom_T=8, status=None, descale_layout=0)
+    for k, v in {**d, **kw}.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), zq.ZQ_ERR_NULL),
+    (dict(k=None), zq.ZQ_ERR_NULL),
+    (dict(v=None), zq.ZQ_ERR_NULL),
+    (dict(out=None), zq.ZQ_ERR_NULL),
+    (dict(cu_seqlens_q=None), zq.ZQ_ERR_NULL),
+    (dict(cu_seqlens_k=None, total_q=0), zq.ZQ_ERR_NULL),
+    (dict(B=0), zq.ZQ_ERR_SHAPE),
+    (dict(B=65536), zq.ZQ_ERR_SHAPE),
+    (dict(total_q=-1), zq.ZQ_ERR_SHAPE),
+    (dict(total_k=-1), zq.ZQ_ERR_SHAPE),
+    (dict(Hq=3), zq.ZQ_ERR_SHAPE),
+    (dict(Hkv=0), zq.ZQ_ERR_SHAPE),
+    (dict(Hq=8192), zq.ZQ_ERR_SHAPE),
+    (dict(total_q=(1 << 31) - 1, Hq=4096), zq.ZQ_ERR_SHAPE),
+    (dict(softmax_scale=float("inf")), zq.ZQ_ERR_SHAPE),
+    (dict(d_qk=64), zq.ZQ_ERR_UNSUPPORTED),
+    (dict(d_v=192), zq.ZQ_ERR_UNSUPPORTED),
+    (dict(dtype=2), zq.ZQ_ERR_UNSUPPORTED),
+    (dict(dtype=1, softmax_mode=2), zq.ZQ_ERR_UNSUPPORTED),
+    (dict(dtype=1, block_scale=2), zq.ZQ_ERR_UNSUPPORTED),
+    (dict(dtype=1, headroom_T=9), zq.ZQ_ERR_UNSUPPORTED),
+    (dict(dtype=1, descale_layout=2), zq.ZQ_ERR_UNSUPPORTED),
+    (dict(q=A + 8), zq.ZQ_ERR_ALIGN),
+    (dict(v=A + 2), zq.ZQ_ERR_ALIGN),
+    (dict(out=A + 4), zq.ZQ_ERR_ALIGN),
+    (dict(lse=A + 4), zq.ZQ_ERR_ALIGN),
+])
+def test_varlen_argument_errors(kw, code):
+    assert zq.zq_attn_varlen_fwd(_varlen(**kw), None) == code
+
+
+def _cu(n):
+    return torch.zeros(n, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("kw,err,msg", [
+    (dict(q=_t(1, 8, 4, 128)), ValueError, "q must be 3-D"),
+    (dict(q=_t(4, 8, 128).transpose(0, 1)), ValueError, "q must be contiguous"),
+    (dict(k=_t(8, 2, 128, dtype=torch.uint8)), TypeError, "all be bfloat16"),
+    (dict(k=_t(8, 2, 192)), ValueError, "head dim"),
+    (dict(v=_t(9, 2, 128)), ValueError, "k's rows"),
+    (dict(v=_t(8, 1, 128)), ValueError, "k's rows"),
+    (dict(cu_seqlens_q=_cu(1), cu_seqlens_k=_cu(1)), ValueError, "B \\+ 1 offsets"),
+    (dict(cu_seqlens_k=_cu(4)), ValueError, "cu_seqlens_k must be"),
+    (dict(cu_seqlens_q=_cu(3).long()), ValueError, "cu_seqlens_q must be"),
+    (dict(cu_seqlens_k=_cu(6)[::2]), ValueError, "cu_seqlens_k must be"),
+    (dict(out=_t(8, 4, 192)), ValueError, "out must have shape"),
+    (dict(lse=_t(8, 4, dtype=torch.float32)), ValueError, "lse must have shape"),
+    (dict(status=_t(1)), ValueError, "status"),
+    (dict(), ValueError, "must be a CUDA tensor"),
+])
+def test_varlen_helper_refuses(kw, err, msg):
+    a = {**dict(q=_t(8, 4, 128), k=_t(8, 2, 128), v=_t(8, 2, 128), cu_seqlens_q=_cu(3), cu_seqlens_k=_cu(3)), **kw}
+    with pytest.raises(err, match=msg):
+        zq.attn_varlen(**a)
+
+
+def test_varlen_helper_refuses_bad_descales():
+    a = dict(q=_t(8, 4, 128, dtype=torch.uint8), k=_t(8, 2, 128, dtype=torch.uint8), v=_t(8, 2, 128, dtype=torch.uint8),
+             cu_seqlens_q=_cu(3), cu_seqlens_k=_cu(3))
+    with pytest.raises(ValueError, match="contiguous float32"):
+        zq.attn_varlen(**a, q_descale=torch.ones(1, dtype=torch.float64))
+    with pytest.raises(ValueError, match="descales must all hold"):
+        zq.attn_varlen(**a, q_descale=torch.ones(4), k_descale=torch.ones(2))
