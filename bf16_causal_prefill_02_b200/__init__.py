@@ -544,16 +544,25 @@ def flash_attn_func(q, k, v, softmax_scale=None, causal=True, return_attn_probs=
     return (out, lse, None) if return_attn_probs else out
 
 
+def _current_device() -> int:
+    return _torch()._C._cuda_getDevice()
+
+
+def _raw_stream(device) -> int:
+    """Handle of the current stream of `device` (an index)."""
+    return _torch()._C._cuda_getCurrentRawStream(device)
+
+
 def _on(device, stream, call):
     """call(raw stream handle) with `device` current and, where `stream` (a
     torch stream or a raw handle) is given, with that stream current, so that
     what the call allocates belongs to the stream that uses it."""
+    if stream is None and _current_device() == device:
+        return call(_raw_stream(device))
     cuda = _torch().cuda
     if stream is None:
-        if cuda.current_device() == device:
-            return call(cuda.current_stream().cuda_stream)
         with cuda.device(device):
-            return call(cuda.current_stream().cuda_stream)
+            return call(_raw_stream(device))
     if not hasattr(stream, "cuda_stream"):
         stream = cuda.ExternalStream(int(stream), device=device) if int(stream) else cuda.default_stream(device)
     elif stream.device.index != device:
@@ -562,10 +571,10 @@ def _on(device, stream, call):
         return call(stream.cuda_stream)
 
 
-def _check_on(device, **tensors):
-    """Every given tensor lives on CUDA device `device` (an index; -1: the host, which is refused)."""
-    for name, t in tensors.items():
-        if t is not None and (t.get_device() != device or device < 0):
+def _check_on(device, *named):
+    """Every given (name, tensor) lives on CUDA device `device` (an index; -1: the host, which is refused)."""
+    for name, t in named:
+        if t is not None and (device < 0 or t.get_device() != device):
             if not t.is_cuda:
                 raise ValueError("%s must be a CUDA tensor" % name)
             raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, device))
@@ -632,12 +641,12 @@ def attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, out=None, lse=None, softmax
     if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
         raise ValueError("status must be an int32 tensor with at least one element")
     device = q.get_device()
-    _check_on(device, q=q, k=k, v=v, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, out=out, lse=lse, q_descale=q_descale,
-              k_descale=k_descale, v_descale=v_descale, status=status)
+    _check_on(device, ("q", q), ("k", k), ("v", v), ("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_k", cu_seqlens_k), ("out", out),
+              ("lse", lse), ("q_descale", q_descale), ("k_descale", k_descale), ("v_descale", v_descale), ("status", status))
 
     def call(s):
-        o = torch.empty((Tq, Hq, dv), dtype=torch.bfloat16, device=q.device) if out is None else out
-        e = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device) if lse is None and return_lse else lse
+        o = q.new_empty((Tq, Hq, dv), dtype=torch.bfloat16) if out is None else out
+        e = q.new_empty((Hq, Tq), dtype=torch.float32) if lse is None and return_lse else lse
         a = zq_varlen_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(e), cu_seqlens_q.data_ptr(),
                            cu_seqlens_k.data_ptr(), B, Tq, Tk, Hq, Hkv, dqk, dv, float(softmax_scale) if softmax_scale else 0.0,
                            int(bool(causal)), dtype, _ptr(q_descale), _ptr(k_descale), _ptr(v_descale), int(softmax_mode),
@@ -670,28 +679,28 @@ def _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale
     else:
         raise TypeError("k_cache and v_cache must both be bfloat16 or both FP8 e4m3")
     pages, page_size, Hkv, dqk = k_cache.shape
-    dv = v_cache.shape[3]
-    if v_cache.shape[:3] != k_cache.shape[:3]:
+    vpages, vpage_size, vHkv, dv = v_cache.shape
+    if vpages != pages or vpage_size != page_size or vHkv != Hkv:
         raise ValueError("v_cache must have k_cache's pages, page size and heads %s, got %s"
                          % (tuple(k_cache.shape[:3]), tuple(v_cache.shape[:3])))
     if block_table.dim() != 2 or block_table.dtype != torch.int32:
         raise ValueError("block_table must be a 2-D int32 tensor (batch, pages per sequence)")
     B, width = block_table.shape
-    if cache_seqlens.dtype != torch.int32 or tuple(cache_seqlens.shape) != (B,) or not cache_seqlens.is_contiguous():
+    if cache_seqlens.dtype != torch.int32 or cache_seqlens.shape != (B,) or not cache_seqlens.is_contiguous():
         raise ValueError("cache_seqlens must be a contiguous int32 tensor of %d lengths" % B)
-    per_head = 0
-    if dtype == ZQ_DTYPE_FP8_E4M3:
+    ks, vs, ts = _row_stride("k_cache", k_cache), _row_stride("v_cache", v_cache), _row_stride("block_table", block_table)
+    device = k_cache.get_device()
+    per_head, kd, vd = 0, None, None
+    if dtype == ZQ_DTYPE_FP8_E4M3 and (k_descale is not None or v_descale is not None):
         for name, t in (("k_descale", k_descale), ("v_descale", v_descale)):
             if t is not None and (t.dtype != torch.float32 or not t.is_contiguous()):
                 raise ValueError("%s must be a contiguous float32 tensor" % name)
         per_head = _descale_layout(1, Hkv, k_descale, v_descale)
-    else:
-        k_descale = v_descale = None
-    ks, vs, ts = _row_stride("k_cache", k_cache), _row_stride("v_cache", v_cache), _row_stride("block_table", block_table)
-    _check_on(k_cache.get_device(), k_cache=k_cache, v_cache=v_cache, block_table=block_table, cache_seqlens=cache_seqlens,
-              k_descale=k_descale, v_descale=v_descale)
+        _check_on(device, ("k_descale", k_descale), ("v_descale", v_descale))
+        kd, vd = _ptr(k_descale), _ptr(v_descale)
+    _check_on(device, ("k_cache", k_cache), ("v_cache", v_cache), ("block_table", block_table), ("cache_seqlens", cache_seqlens))
     return zq_paged_kv(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, block_table.data_ptr(), cache_seqlens.data_ptr(),
-                       _ptr(k_descale), _ptr(v_descale), ts, width, pages, page_size, B, Hkv, dqk, dv, dtype, per_head)
+                       kd, vd, ts, width, pages, page_size, B, Hkv, dqk, dv, dtype, per_head), device, B, Hkv, dqk, dv
 
 
 def kv_append(k, v, k_cache, v_cache, block_table, cache_seqlens, cu_seqlens=None, k_descale=None, v_descale=None, stream=None):
@@ -706,24 +715,23 @@ def kv_append(k, v, k_cache, v_cache, block_table, cache_seqlens, cu_seqlens=Non
     onwards of the pages in block_table[b]; cache_seqlens is not advanced.
     Returns (k_cache, v_cache)."""
     torch = _torch()
-    c = _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale)
+    c, device, B, Hkv, dqk, dv = _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale)
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
         raise TypeError("k and v must be bfloat16")
-    if k.dim() != 3 or tuple(k.shape[1:]) != (c.Hkv, c.d_qk):
-        raise ValueError("k must have shape (tokens, %d, %d), got %s" % (c.Hkv, c.d_qk, tuple(k.shape)))
-    T = k.shape[0]
-    if tuple(v.shape) != (T, c.Hkv, c.d_v):
-        raise ValueError("v must have shape %s, got %s" % ((T, c.Hkv, c.d_v), tuple(v.shape)))
+    T = k.shape[0] if k.dim() else 0
+    if k.shape != (T, Hkv, dqk):
+        raise ValueError("k must have shape (tokens, %d, %d), got %s" % (Hkv, dqk, tuple(k.shape)))
+    if v.shape != (T, Hkv, dv):
+        raise ValueError("v must have shape %s, got %s" % ((T, Hkv, dv), tuple(v.shape)))
     if cu_seqlens is None:
-        if T != c.B:
-            raise ValueError("without cu_seqlens there is one token for each of the %d sequences, got %d" % (c.B, T))
-    elif cu_seqlens.dtype != torch.int32 or tuple(cu_seqlens.shape) != (c.B + 1,) or not cu_seqlens.is_contiguous():
-        raise ValueError("cu_seqlens must be a contiguous int32 tensor of %d offsets" % (c.B + 1))
-    device = k_cache.get_device()
-    _check_on(device, k=k, v=v, cu_seqlens=cu_seqlens)
+        if T != B:
+            raise ValueError("without cu_seqlens there is one token for each of the %d sequences, got %d" % (B, T))
+    elif cu_seqlens.dtype != torch.int32 or cu_seqlens.shape != (B + 1,) or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous int32 tensor of %d offsets" % (B + 1))
     ks, vs = _row_stride("k", k), _row_stride("v", v)
-    _on(device, stream, lambda s: _check(zq_kv_append(c, k.data_ptr(), v.data_ptr(), ks, vs, _ptr(cu_seqlens), T, s),
-                                         "zq_kv_append"))
+    _check_on(device, ("k", k), ("v", v), ("cu_seqlens", cu_seqlens))
+    kp, vp, cp = k.data_ptr(), v.data_ptr(), _ptr(cu_seqlens)
+    _on(device, stream, lambda s: _check(zq_kv_append(c, kp, vp, ks, vs, cp, T, s), "zq_kv_append"))
     return k_cache, v_cache
 
 
@@ -735,29 +743,28 @@ def attn_decode(q, k_cache, v_cache, block_table, cache_seqlens, out=None, lse=N
     with cache_seqlens (int32, B) keys in each sequence.
     Returns (out bf16 (B,Hq,d_v), lse fp32 (B,Hq) or None)."""
     torch = _torch()
-    c = _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale)
+    c, device, B, Hkv, dqk, dv = _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale)
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be bfloat16")
-    if q.dim() != 3 or q.shape[0] != c.B or q.shape[2] != c.d_qk:
-        raise ValueError("q must have shape (%d, heads, %d), got %s" % (c.B, c.d_qk, tuple(q.shape)))
-    B, Hq = q.shape[0], q.shape[1]
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != dqk:
+        raise ValueError("q must have shape (%d, heads, %d), got %s" % (B, dqk, tuple(q.shape)))
+    Hq = q.shape[1]
     if out is not None:
-        _check_buffer("out", out, (B, Hq, c.d_v), torch.bfloat16)
+        _check_buffer("out", out, (B, Hq, dv), torch.bfloat16)
     if lse is not None:
         _check_buffer("lse", lse, (B, Hq), torch.float32)
     nbytes = zq_decode_workspace_bytes()
     if workspace is not None and (workspace.numel() * workspace.element_size() < nbytes or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous and hold zq_decode_workspace_bytes() bytes")
-    device = k_cache.get_device()
-    _check_on(device, q=q, out=out, lse=lse, workspace=workspace)
     qs = _row_stride("q", q)
+    _check_on(device, ("q", q), ("out", out), ("lse", lse), ("workspace", workspace))
+    scale = float(softmax_scale) if softmax_scale else 0.0
 
     def call(s):
-        o = torch.empty((B, Hq, c.d_v), dtype=torch.bfloat16, device=q.device) if out is None else out
-        e = torch.empty((B, Hq), dtype=torch.float32, device=q.device) if lse is None and return_lse else lse
-        w = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if workspace is None else workspace
-        _check(zq_attn_decode(c, q.data_ptr(), qs, Hq, float(softmax_scale) if softmax_scale else 0.0, o.data_ptr(), _ptr(e),
-                              w.data_ptr(), s), "zq_attn_decode")
+        o = q.new_empty((B, Hq, dv)) if out is None else out
+        e = q.new_empty((B, Hq), dtype=torch.float32) if lse is None and return_lse else lse
+        w = q.new_empty(nbytes, dtype=torch.uint8) if workspace is None else workspace
+        _check(zq_attn_decode(c, q.data_ptr(), qs, Hq, scale, o.data_ptr(), _ptr(e), w.data_ptr(), s), "zq_attn_decode")
         return o, e
 
     return _on(device, stream, call)

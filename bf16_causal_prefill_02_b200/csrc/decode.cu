@@ -10,15 +10,18 @@
 //     from memory once for all of them.  The rows that a small group leaves
 //     empty cost tensor work that is not what bounds the kernel.
 //   * The cache's length is split.  All key tiles of all (sequence, kv head)
-//     pairs form one line that is cut into equal pieces, one per CTA, so
+//     pairs form one line that is cut into equal pieces, one per warp, so
 //     ragged lengths cost no balance.  A piece that holds a whole (sequence,
 //     head) writes the output; a cut one writes (m, l, O) to the workspace and
 //     decode_join_kernel joins the parts: M = max m_j, l = sum l_j 2^(m_j - M),
 //     o = sum O_j 2^(m_j - M) / l.  The order is fixed, so runs repeat bit for
 //     bit.
-//   * Inside a CTA every warp streams its own keys through its own ring of
-//     cp.async stages (no block-wide barrier in the loop), with its own
-//     running maximum and sum; the four warps are joined at a segment's end.
+//   * A warp streams its keys through a ring of cp.async stages of its own and
+//     waits for no other warp: the start and the end of one's segment overlap
+//     the other seven's streams on the SM.
+//   * With at most 8 query heads per kv head (SMALL) the product's other 8
+//     rows carry what the rounding of the weights to bf16 leaves out: P = P_hi
+//     + P_lo costs no further product, and rows 8-15 need no exponentials.
 // Keys past the end, and keys whose page is not in the cache, are not read:
 // their rows are filled with zeros and masked, so what lies there (NaN too)
 // does not matter.
@@ -33,8 +36,15 @@ namespace {
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kRows = 16;      // query heads per head tile
-constexpr int kMaxCtas = 512;  // pieces the workspace has room for
+constexpr int kMaxCtas = 320;  // the workspace has room for their pieces
+constexpr int kMaxPieces = kMaxCtas * kDecWarps;
 constexpr int kCtasPerSm = 2;
+constexpr int kSlot = kRows * 128 + 2 * kRows;  // floats of a part: O, then (m, l) per row
+// What a segment costs beyond its tiles (first loads, last stores), in tiles:
+// a piece of many short segments gets fewer of them.
+constexpr int kSegmentCost = 2;
+constexpr int kJoinWarps = 8;
+constexpr int kJoinAlone = 8;  // parts that one warp joins by itself
 
 struct DecodeParams {
   PagedKV c;
@@ -45,16 +55,15 @@ struct DecodeParams {
   float scale;
   int Hq, group, head_tiles;
   // workspace: who cuts what, then the parts
-  int4* cut;     // [grid] {sequence, flat head tile, parts, 0} of the segment this CTA starts and does not finish
-  float* part;   // [grid][2][kRows * dv + 2 * kRows]: slot 0 a segment begun by an earlier CTA, slot 1 one left to later CTAs
+  int4* cut;     // [piece] {sequence, flat head tile, parts, 0} of the segment that this piece begins and does not finish
+  float* part;   // [piece][2][kSlot]: slot 0 a segment begun by an earlier piece, slot 1 one left to later pieces
 };
 
 template <int DQK, int FP8>
 struct DecGeo {
   static constexpr int DV = 128;
   static constexpr int ES = FP8 ? 1 : 2;
-  static constexpr int KW = FP8 ? 32 : 16;              // keys per warp and step
-  static constexpr int TK = KW * kDecWarps;             // keys per tile of the line
+  static constexpr int KW = FP8 ? 32 : 16;              // keys per tile (one step of a warp)
   static constexpr int KCH = DQK * ES / 16;             // 16-byte pieces per key row
   static constexpr int VCH = DV * ES / 16;
   static constexpr int KBYTES = KW * KCH * 16;
@@ -62,10 +71,8 @@ struct DecGeo {
   static constexpr int STAGE = KBYTES + VBYTES;
   static constexpr int NS = DQK == 128 ? 3 : 2;         // stages that fit 113 KB (two CTAs per SM)
   static constexpr int RING = NS * STAGE;               // bytes per warp
-  static constexpr int JOIN = kRows * DV * 4;           // a warp's O at a segment's end, over its ring
-  static constexpr int SMEM = kDecWarps * RING + kDecWarps * kRows * 8;
+  static constexpr int SMEM = kDecWarps * RING;
   static constexpr int QK_STEPS = DQK / 16;
-  static_assert(RING >= JOIN, "O fits the ring");
   static_assert(SMEM <= 113 * 1024, "two CTAs per SM");
   // place of piece ch of row r: pieces of eight rows fall in different banks
   __device__ static constexpr uint32_t at_k(int r, int ch) {
@@ -79,30 +86,36 @@ __device__ __forceinline__ int keys_of(const PagedKV& c, int b) {
   return (int)min((int64_t)max(c.seqlens[b], 0), cap);
 }
 
-template <int DQK, int FP8>
+template <int DQK, int FP8, int SMALL>
 __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const DecodeParams p) {
   using G = DecGeo<DQK, FP8>;
   constexpr int DV = G::DV, KW = G::KW, NS = G::NS;
+  constexpr int HF = SMALL ? 1 : 2;  // rows quad, and quad + 8 unless SMALL
   constexpr unsigned kFull = 0xffffffffu;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t scan[kDecWarps + 1];
-  __shared__ int64_t first_off;
-  __shared__ int first_b;
+  __shared__ int64_t scan[kDecWarps];
+  __shared__ int64_t first_off[kDecWarps];
+  __shared__ int first_b[kDecWarps];
   const PagedKV& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane >> 2, ql = lane & 3;
   const int heads = c.Hkv * p.head_tiles;
   launch_dependents();
 
-  // ---- this CTA's piece [x, x1) of the line: b outermost, then the flat head tile, then the key tile
-  int64_t x, x1, line;
+  // ---- the line: b outermost, then the flat head tile, then kSegmentCost
+  // places without a tile and the key tiles
+  auto places = [&](int b) -> int64_t {
+    const int n = keys_of(c, b);
+    return n > 0 ? (int64_t)((n + KW - 1) / KW + kSegmentCost) * heads : 0;
+  };
+  int64_t x = 0, x1 = 0, line = 0;  // this warp's piece
   int pieces;
+  const int piece = warp * gridDim.x + blockIdx.x;  // (few pieces are spread over the SMs)
   {
     const int per = (c.B + kDecThreads - 1) / kDecThreads;
     const int b0 = min((int)threadIdx.x * per, c.B), b1 = min(b0 + per, c.B);
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += (keys_of(c, b) + G::TK - 1) / G::TK;
-    mine *= heads;
+    for (int b = b0; b < b1; ++b) mine += places(b);
     int64_t sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -111,32 +124,35 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
     }
     if (lane == 31) scan[warp] = sum;
     __syncthreads();
-    int64_t before = 0, total = 0;
+    int64_t before = 0;
 #pragma unroll
     for (int w = 0; w < kDecWarps; ++w) {
       if (w < warp) before += scan[w];
-      total += scan[w];
+      line += scan[w];
     }
-    // no more pieces than tiles, so that none is empty
-    pieces = (int)min((int64_t)gridDim.x, total);
-    line = total;
-    x = x1 = 0;
-    if ((int)blockIdx.x < pieces) {
-      x = total * blockIdx.x / pieces;
-      x1 = total * (blockIdx.x + 1) / pieces;
-    }
-    int64_t at = before + sum - mine;  // line position of this thread's first sequence
-    if (x < x1 && x >= at && x < at + mine) {
+    // no more pieces than places, so that none is empty
+    pieces = (int)min((int64_t)gridDim.x * kDecWarps, line);
+    const int64_t at0 = before + sum - mine;  // place of this thread's first sequence
+    for (int w = 0; w < kDecWarps; ++w) {
+      const int pw = w * gridDim.x + blockIdx.x;
+      if (pw >= pieces) break;
+      const int64_t y = line * pw / pieces;
+      if (y < at0 || y >= at0 + mine) continue;
+      int64_t at = at0;
       int b = b0;
       for (;; ++b) {
-        const int64_t n = (int64_t)((keys_of(c, b) + G::TK - 1) / G::TK) * heads;
-        if (x < at + n) break;
+        const int64_t n = places(b);
+        if (y < at + n) break;
         at += n;
       }
-      first_b = b;
-      first_off = x - at;
+      first_b[w] = b;
+      first_off[w] = y - at;
     }
     __syncthreads();
+    if (piece < pieces) {
+      x = line * piece / pieces;
+      x1 = line * (piece + 1) / pieces;
+    }
   }
   // sequences without keys: 0 and -inf
   for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
@@ -147,35 +163,43 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
       for (int i = threadIdx.x; i < p.Hq; i += kDecThreads) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
   }
 
-  uint8_t* const ring = smem + warp * G::RING;
-  const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-  float2* const stats = reinterpret_cast<float2*>(smem + kDecWarps * G::RING);  // [warp][row] (m, l)
-  bool cut = false;  // a segment of this piece is left to later CTAs
+  const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(smem + warp * G::RING));
+  int4 cut = make_int4(0, 0, 0, 0);  // the segment of this piece that is left to later ones
 
-  int b = x < x1 ? first_b : 0;
-  int64_t off = x < x1 ? first_off : 0;
+  int b = x < x1 ? first_b[warp] : 0;
+  int64_t off = x < x1 ? first_off[warp] : 0;
   while (x < x1) {
     const int len = keys_of(c, b);
-    const int tiles = (len + G::TK - 1) / G::TK;
-    if (off >= (int64_t)tiles * heads) {
-      off -= (int64_t)tiles * heads;
+    const int tiles = (len + KW - 1) / KW, span = tiles + kSegmentCost;
+    if (len == 0 || off >= (int64_t)span * heads) {
+      off -= len == 0 ? 0 : (int64_t)span * heads;
       ++b;
       continue;
     }
-    const int fh = (int)(off / tiles), t0 = (int)(off % tiles);
-    const int steps = (int)min((int64_t)(tiles - t0), x1 - x);
+    const int fh = (int)(off / span), r0 = (int)(off % span);
+    const int r1 = (int)min((int64_t)span, r0 + (x1 - x));
+    const int64_t start = x - r0;  // the (sequence, head)'s first place
+    x += r1 - r0;
+    off += r1 - r0;
+    const int t0 = max(r0 - kSegmentCost, 0);
+    const int steps = r1 - kSegmentCost - t0;
+    if (steps <= 0) continue;
     const int g = fh / p.head_tiles, ht = fh % p.head_tiles;
     const int h0 = g * p.group + ht * kRows;          // first query head of the tile
     const int rows = min(kRows, p.group - ht * kRows);  // query heads in it
 
     // ---- queries as A fragments: rows quad and quad + 8
     uint32_t qa[G::QK_STEPS][4];
+    if constexpr (SMALL) {
+#pragma unroll
+      for (int ks = 0; ks < G::QK_STEPS; ++ks) qa[ks][1] = qa[ks][3] = 0u;
+    }
     const float c2 = p.scale * (FP8 && c.k_descale ? c.k_descale[c.descale_per_head ? g : 0] : 1.0f) * 1.4426950408889634f;
     float cr[2] = {c2, c2};
     {
       const __nv_bfloat16* qrow = p.q + b * p.q_stride + (int64_t)h0 * DQK;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+      for (int hf = 0; hf < HF; ++hf) {
         const int r = quad + hf * 8;
         const bool there = r < rows;
         const uint32_t* src = reinterpret_cast<const uint32_t*>(qrow + (int64_t)r * DQK);
@@ -216,16 +240,16 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
       }
     }
 
-    // ---- the segment's keys: warp w takes keys [w KW, (w + 1) KW) of every tile
+    // ---- the segment's keys
     const int32_t* table = c.table + b * c.table_stride;
-    const int key0 = t0 * G::TK + warp * KW;
+    const int key0 = t0 * KW;
     const char* kbase = c.k + (int64_t)g * (DQK * G::ES);
     const char* vbase = c.v + (int64_t)g * (DV * G::ES);
     const int64_t krow = (int64_t)c.Hkv * (DQK * G::ES), vrow = (int64_t)c.Hkv * (DV * G::ES);
     const int page_mask = (1 << c.page_shift) - 1;
     // the page of key (step, lane), or -1: not there
     auto page_at = [&](int step) -> int {
-      const int key = key0 + step * G::TK + lane;
+      const int key = key0 + step * KW + lane;
       int pg = -1;
       if (lane < KW && step < steps && key < len) pg = table[key >> c.page_shift];
       return (unsigned)pg < (unsigned)c.num_pages ? pg : -1;
@@ -237,7 +261,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
       for (int i = 0; i < NS; ++i)
         if (i == s) have[i] = vm;
       const uint32_t sk = ring_u + s * G::STAGE, sv = sk + G::KBYTES;
-      const int kb = key0 + step * G::TK;
+      const int kb = key0 + step * KW;
 #pragma unroll
       for (int i = 0; i < KW * G::KCH / 32; ++i) {
         const int idx = i * 32 + lane, r = idx / G::KCH, ch = idx % G::KCH;
@@ -301,44 +325,53 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
         }
         // log2 domain, mask
         const unsigned vm = have[s];
-        float mx[2] = {-INFINITY, -INFINITY};
+        float mx[HF];
 #pragma unroll
-        for (int n = 0; n < KW / 8; ++n)
+        for (int hf = 0; hf < HF; ++hf) {
+          mx[hf] = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sc[n][i] *= cr[i >> 1];
-            if (!((vm >> (n * 8 + 2 * ql + (i & 1))) & 1u)) sc[n][i] = -INFINITY;
-            mx[i >> 1] = fmaxf(mx[i >> 1], sc[n][i]);
-          }
+          for (int n = 0; n < KW / 8; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float& z = sc[n][2 * hf + i];
+              z *= cr[hf];
+              if (!((vm >> (n * 8 + 2 * ql + i)) & 1u)) z = -INFINITY;
+              mx[hf] = fmaxf(mx[hf], z);
+            }
+        }
         // the reference moves when a score passes it by 8 (weights stay below 2^8)
-        if (__any_sync(kFull, mx[0] > ref[0] + 8.0f || mx[1] > ref[1] + 8.0f)) {
+        if (__any_sync(kFull, mx[0] > ref[0] + 8.0f || mx[HF - 1] > ref[HF - 1] + 8.0f)) {
+          float f[2];
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
+          for (int hf = 0; hf < HF; ++hf) {
             float m = fmaxf(mx[hf], __shfl_xor_sync(kFull, mx[hf], 1));
             m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
             const float nref = fmaxf(ref[hf], m);
-            const float f = (nref == -INFINITY || nref == ref[hf]) ? 1.0f : ex2_approx(ref[hf] - nref);
+            f[hf] = (nref == -INFINITY || nref == ref[hf]) ? 1.0f : ex2_approx(ref[hf] - nref);
             ref[hf] = nref;
-            l[hf] *= f;
-#pragma unroll
-            for (int n = 0; n < DV / 8; ++n) {
-              o[n][2 * hf] *= f;
-              o[n][2 * hf + 1] *= f;
-            }
+            l[hf] *= f[hf];
           }
+          if (SMALL) f[1] = f[0];  // the low parts of the same heads
+#pragma unroll
+          for (int n = 0; n < DV / 8; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n][i] *= f[i >> 1];
         }
-        const float nb[2] = {ref[0] == -INFINITY ? 0.0f : ref[0], ref[1] == -INFINITY ? 0.0f : ref[1]};
         uint32_t pa[KW / 16][4];
 #pragma unroll
-        for (int n = 0; n < KW / 8; ++n) {
+        for (int hf = 0; hf < HF; ++hf) {
+          const float nb = ref[hf] == -INFINITY ? 0.0f : ref[hf];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sc[n][i] = ex2_approx(sc[n][i] - nb[i >> 1]);
-            l[i >> 1] += sc[n][i];
+          for (int n = 0; n < KW / 8; ++n) {
+            const float p0 = ex2_approx(sc[n][2 * hf] - nb), p1 = ex2_approx(sc[n][2 * hf + 1] - nb);
+            l[hf] += p0 + p1;
+            const uint32_t w = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+            pa[n / 2][(n & 1) * 2 + hf] = w;
+            if constexpr (SMALL && !FP8)
+              pa[n / 2][(n & 1) * 2 + 1] = pack_bf16x2(p0 - __uint_as_float(w << 16), p1 - __uint_as_float(w & 0xffff0000u));
+            else if constexpr (SMALL)
+              pa[n / 2][(n & 1) * 2 + 1] = 0u;
           }
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-            pa[n / 2][(n & 1) * 2 + hf] = FP8 ? pack_f16x2(sc[n][2 * hf], sc[n][2 * hf + 1]) : pack_bf16x2(sc[n][2 * hf], sc[n][2 * hf + 1]);
         }
         // O += P V
         if constexpr (!FP8) {
@@ -371,15 +404,42 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
     cp_async_wait<0>();
     __syncwarp();
 
-    // ---- join the warps: every warp's O (and m, l) through its own ring
+    // ---- the segment's end: to the output, or to this piece's slot
+    const bool begins = t0 == 0, ends = t0 + steps == tiles;
+    const float vds = FP8 && c.v_descale ? c.v_descale[c.descale_per_head ? g : 0] : 1.0f;
+    float* const slot = p.part + ((int64_t)piece * 2 + (begins ? 1 : 0)) * kSlot;
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
+    for (int hf = 0; hf < HF; ++hf) {
       l[hf] += __shfl_xor_sync(kFull, l[hf], 1);
       l[hf] += __shfl_xor_sync(kFull, l[hf], 2);
+      if (SMALL && !FP8) {
+#pragma unroll
+        for (int n = 0; n < DV / 8; ++n) {
+          o[n][0] += o[n][2];
+          o[n][1] += o[n][3];
+        }
+      }
       const int r = quad + hf * 8;
-      if (r < rows) {
-        if (ql == 0) stats[warp * kRows + r] = make_float2(ref[hf], l[hf]);
-        float* dst = reinterpret_cast<float*>(ring) + r * DV;
+      if (r >= rows) continue;
+      if (begins && ends) {
+        const int64_t row = (int64_t)b * p.Hq + h0 + r;
+        // no key was there (l = 0): 0 and -inf; NaN stays NaN
+        const bool empty = l[hf] == 0.0f;
+        const float inv = vds / l[hf];
+        auto two = [&](float a, float z) { return empty ? 0u : pack_bf16x2(a * inv, z * inv); };
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * DV);
+        if constexpr (!FP8) {
+#pragma unroll
+          for (int n = 0; n < DV / 8; ++n) dst[n * 4 + ql] = two(o[n][2 * hf], o[n][2 * hf + 1]);
+        } else {
+#pragma unroll
+          for (int ch = 0; ch < DV / 16; ++ch)
+            reinterpret_cast<uint2*>(dst)[ch * 4 + ql] =
+                make_uint2(two(o[2 * ch][2 * hf], o[2 * ch + 1][2 * hf]), two(o[2 * ch][2 * hf + 1], o[2 * ch + 1][2 * hf + 1]));
+        }
+        if (p.lse && ql == 0) p.lse[row] = empty ? -INFINITY : (ref[hf] + log2f(l[hf])) * 0.6931471805599453f;
+      } else {
+        float* dst = slot + r * DV;
         if constexpr (!FP8) {
 #pragma unroll
           for (int n = 0; n < DV / 8; ++n)
@@ -390,82 +450,25 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
             *reinterpret_cast<float4*>(dst + ch * 16 + 4 * ql) =
                 make_float4(o[2 * ch][2 * hf], o[2 * ch + 1][2 * hf], o[2 * ch][2 * hf + 1], o[2 * ch + 1][2 * hf + 1]);
         }
-      }
-    }
-    __syncthreads();
-    const bool begins = t0 == 0, ends = t0 + steps == tiles;
-    const float vds = FP8 && c.v_descale ? c.v_descale[c.descale_per_head ? g : 0] : 1.0f;
-    float* slot = p.part + ((int64_t)blockIdx.x * 2 + (begins ? 1 : 0)) * (kRows * DV + 2 * kRows);
-    for (int r = 0; r < rows; ++r) {
-      float2 st[kDecWarps];
-      float m = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        st[w] = stats[w * kRows + r];
-        m = fmaxf(m, st[w].x);
-      }
-      const float mb = m == -INFINITY ? 0.0f : m;
-      float acc = 0.0f, sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        const float f = ex2_approx(st[w].x - mb);
-        sum += st[w].y * f;
-        acc += reinterpret_cast<const float*>(smem + w * G::RING)[r * DV + threadIdx.x] * f;
-      }
-      if (begins && ends) {
-        const int64_t row = (int64_t)b * p.Hq + h0 + r;
-        // no key was there (l = 0): 0 and -inf; NaN stays NaN
-        const bool empty = sum == 0.0f;
-        p.out[row * DV + threadIdx.x] = __float2bfloat16(empty ? 0.0f : acc * (vds / sum));
-        if (p.lse && threadIdx.x == 0) p.lse[row] = empty ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
-      } else {
-        slot[r * DV + threadIdx.x] = acc;
-        if (threadIdx.x == 0) {
-          slot[kRows * DV + 2 * r] = m;
-          slot[kRows * DV + 2 * r + 1] = sum;
-        }
+        if (ql == 0) *reinterpret_cast<float2*>(slot + kRows * DV + 2 * r) = make_float2(ref[hf], l[hf]);
       }
     }
     if (begins && !ends) {
-      cut = true;
-      if (threadIdx.x == 0) {
-        // its parts: this CTA's and those up to the one that holds its last tile
-        const int64_t last = x + tiles - 1;
-        // the CTA of position y: the largest j with floor(line * j / pieces) <= y
-        const int64_t j = ((last + 1) * pieces - 1) / line;
-        p.cut[blockIdx.x] = make_int4(b, fh, (int)(j - blockIdx.x) + 1, 0);
-      }
+      // its parts: this piece's and those up to the one of its last place.
+      // The piece of place y is the largest j with floor(line * j / pieces) <= y.
+      const int64_t j = ((start + span) * pieces - 1) / line;
+      cut = make_int4(b, fh, (int)(j - piece) + 1, 0);
     }
-    __syncthreads();  // the rings may be filled again
-    x += steps;
-    off += steps;
+    __syncwarp();
   }
-  if (!cut && threadIdx.x == 0) p.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (lane == 0) p.cut[piece] = cut;
 }
 
-// Joins the parts of the (sequence, head tile) that CTA blockIdx.x began and
-// did not finish; blockIdx.y is the query head in it.  Warp w takes parts w,
-// w + 4, ...; a lane holds four channels.
-__global__ void __launch_bounds__(kDecThreads) decode_join_kernel(const DecodeParams p) {
-  constexpr int DV = 128;
-  constexpr int SLOT = kRows * DV + 2 * kRows;
-  __shared__ float4 acc_s[kDecWarps][32];
-  __shared__ float2 stat_s[kDecWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y;
-  wait_previous_kernel();
-  const int4 d = p.cut[blockIdx.x];
-  if (d.z == 0) return;
-  const int b = d.x, g = d.y / p.head_tiles, ht = d.y % p.head_tiles;
-  if (r >= min(kRows, p.group - ht * kRows)) return;
-  auto slot = [&](int j) {  // part j: the beginning is in slot 1 of this CTA, the rest in slot 0 of those after it
-    return p.part + ((int64_t)(blockIdx.x + j) * 2 + (j == 0 ? 1 : 0)) * SLOT;
-  };
+// Running (m, l, O) of a row, a lane's four channels of O.
+struct Part {
   float m = -INFINITY, l = 0.0f;
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int j = warp; j < d.z; j += kDecWarps) {
-    const float* s = slot(j);
-    const float2 st = *reinterpret_cast<const float2*>(s + kRows * DV + 2 * r);
-    const float4 v = reinterpret_cast<const float4*>(s + r * DV)[lane];
+  __device__ __forceinline__ void add(float2 st, float4 v) {
     const float nm = fmaxf(m, st.x), nb = nm == -INFINITY ? 0.0f : nm;
     const float fa = ex2_approx(m - nb), fb = ex2_approx(st.x - nb);
     l = l * fa + st.y * fb;
@@ -475,50 +478,84 @@ __global__ void __launch_bounds__(kDecThreads) decode_join_kernel(const DecodePa
     a.w = a.w * fa + v.w * fb;
     m = nm;
   }
-  acc_s[warp][lane] = a;
-  if (lane == 0) stat_s[warp] = make_float2(m, l);
-  __syncthreads();
-  if (warp != 0) return;
-  float M = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, stat_s[w].x);
-  const float mb = M == -INFINITY ? 0.0f : M;
-  float L = 0.0f;
-  a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) {
-    const float f = ex2_approx(stat_s[w].x - mb);
-    const float4 v = acc_s[w][lane];
-    L += stat_s[w].y * f;
-    a.x += v.x * f;
-    a.y += v.y * f;
-    a.z += v.z * f;
-    a.w += v.w * f;
+};
+
+// Joins the parts of the segments that were cut; blockIdx.y is the query head
+// in the head tile.  A warp joins the few parts of its own piece's segment
+// alone; the parts of a segment with many are shared by the block's warps.
+__global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const DecodeParams p, int pieces) {
+  constexpr int DV = 128;
+  __shared__ float4 acc_s[kJoinWarps][32];
+  __shared__ float2 stat_s[kJoinWarps];
+  __shared__ int4 cut_s[kJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y;
+  const int mine = blockIdx.x * kJoinWarps + warp;
+  wait_previous_kernel();
+  // slot 1 of the piece that begins the segment, slot 0 of those after it
+  auto read = [&](Part& t, int piece, int first, int step, int parts) {
+#pragma unroll 4
+    for (int j = first; j < parts; j += step) {
+      const float* s = p.part + ((int64_t)(piece + j) * 2 + (j == 0 ? 1 : 0)) * kSlot;
+      t.add(*reinterpret_cast<const float2*>(s + kRows * DV + 2 * r), reinterpret_cast<const float4*>(s + r * DV)[lane]);
+    }
+  };
+  auto write = [&](const Part& t, int4 d) {
+    const int g = d.y / p.head_tiles, ht = d.y % p.head_tiles;
+    const bool empty = t.l == 0.0f;
+    const float vds = p.c.dtype == 1 && p.c.v_descale ? p.c.v_descale[p.c.descale_per_head ? g : 0] : 1.0f;
+    const float inv = vds / t.l;
+    const int64_t row = (int64_t)d.x * p.Hq + g * p.group + ht * kRows + r;
+    reinterpret_cast<uint2*>(p.out + row * DV)[lane] =
+        empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(t.a.x * inv, t.a.y * inv), pack_bf16x2(t.a.z * inv, t.a.w * inv));
+    if (p.lse && lane == 0) p.lse[row] = empty ? -INFINITY : (t.m + log2f(t.l)) * 0.6931471805599453f;
+  };
+  int4 d = mine < pieces ? p.cut[mine] : make_int4(0, 0, 0, 0);
+  if (r >= min(kRows, p.group - (d.y % p.head_tiles) * kRows)) d.z = 0;
+  if (d.z > 0 && d.z <= kJoinAlone) {
+    Part t;
+    read(t, mine, 0, 1, d.z);
+    write(t, d);
   }
-  const bool empty = L == 0.0f;
-  const float vds = p.c.dtype == 1 && p.c.v_descale ? p.c.v_descale[p.c.descale_per_head ? g : 0] : 1.0f;
-  const float inv = empty ? 0.0f : vds / L;
-  const int64_t row = (int64_t)b * p.Hq + g * p.group + ht * kRows + r;
-  uint2 w2 = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-  if (empty) w2 = make_uint2(0u, 0u);
-  reinterpret_cast<uint2*>(p.out + row * DV)[lane] = w2;
-  if (p.lse && lane == 0) p.lse[row] = empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  if (lane == 0) cut_s[warp] = d;
+  __syncthreads();
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const int4 e = cut_s[w];
+    if (e.z <= kJoinAlone) continue;
+    Part t;
+    read(t, blockIdx.x * kJoinWarps + w, warp, kJoinWarps, e.z);
+    acc_s[warp][lane] = t.a;
+    if (lane == 0) stat_s[warp] = make_float2(t.m, t.l);
+    __syncthreads();
+    if (warp == 0) {
+      Part all;
+#pragma unroll
+      for (int v = 0; v < kJoinWarps; ++v) all.add(stat_s[v], acc_s[v][lane]);
+      write(all, e);
+    }
+    __syncthreads();
+  }
 }
 
-template <int DQK, int FP8>
-cudaError_t launch_variant(DecodeParams& p, cudaStream_t st, int grid) {
+template <int DQK, int FP8, int SMALL>
+cudaError_t launch_kernel(const DecodeParams& p, cudaStream_t st, int grid) {
   using G = DecGeo<DQK, FP8>;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<DQK, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
+  auto kern = decode_kernel<DQK, FP8, SMALL>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
   if (e != cudaSuccess) return e;
-  decode_kernel<DQK, FP8><<<grid, kDecThreads, G::SMEM, st>>>(p);
+  kern<<<grid, kDecThreads, G::SMEM, st>>>(p);
   return cudaGetLastError();
 }
 
-constexpr size_t kCutBytes = (size_t)kMaxCtas * 16;
+template <int DQK, int FP8>
+cudaError_t launch_variant(const DecodeParams& p, cudaStream_t st, int grid) {
+  return p.group <= 8 ? launch_kernel<DQK, FP8, 1>(p, st, grid) : launch_kernel<DQK, FP8, 0>(p, st, grid);
+}
+
+constexpr size_t kCutBytes = (size_t)kMaxPieces * 16;
 
 }  // namespace
 
-size_t decode_workspace_bytes() { return kCutBytes + (size_t)kMaxCtas * 2 * (kRows * 128 + 2 * kRows) * 4; }
+size_t decode_workspace_bytes() { return kCutBytes + (size_t)kMaxPieces * 2 * kSlot * 4; }
 
 cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t st, int num_sms) {
   DecodeParams p;
@@ -541,15 +578,16 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t st, int num_sms) {
     e = a.c.dqk == 128 ? launch_variant<128, 0>(p, st, grid) : launch_variant<192, 0>(p, st, grid);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.group < kRows ? p.group : kRows));
-  cfg.blockDim = dim3(kDecThreads);
+  const int pieces = grid * kDecWarps;
+  cfg.gridDim = dim3((unsigned)((pieces + kJoinWarps - 1) / kJoinWarps), (unsigned)(p.group < kRows ? p.group : kRows));
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel, p);
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel, p, pieces);
 }
 
 }  // namespace zq

@@ -484,7 +484,7 @@ ZQ_API int zq_kv_append(const zq_paged_kv* cache, const void* k, const void* v, 
 ZQ_API int zq_attn_decode(const zq_paged_kv* cache, const void* q, int64_t q_stride, int Hq,
                           float softmax_scale, void* out, float* lse, void* workspace, void* stream);
 
-/* Bytes of device scratch zq_attn_decode needs (a constant, about 9 MB). */
+/* Bytes of device scratch zq_attn_decode needs (a constant, about 21 MB). */
 ZQ_API size_t zq_decode_workspace_bytes(void);
 
 /* zq_debug_exp2 -- y[i] = 2^x[i] by the kernels' software exp2 (degree 3 or
