@@ -5,10 +5,14 @@
 //
 // Bound by reading the cache once: n * Hkv * (d_qk + d_v) elements against
 // 2 * (Hq / Hkv) * (d_qk + d_v) operations a key.  So:
-//   * The query heads of a kv head (16 at most; more go in further head
-//     tiles) are the 16 rows of m16n8k16 products, and a key or value is read
-//     from memory once for all of them.  The rows that a small group leaves
-//     empty cost tensor work that is not what bounds the kernel.
+//   * The query heads of a kv head share every key and value that is read.
+//     The products are m16n8k16 with the long side on the 16: S^T = K Q^T (16
+//     keys by 8 heads) and O^T = V^T P^T (16 channels by 8 heads), so a group of
+//     up to 8 heads leaves little of them empty; up to 16 take two products
+//     side by side (NT = 2), larger groups further head tiles.
+//   * P^T is rounded to bf16 twice, P = P_hi + P_lo, over a bf16 cache: the
+//     tensor work is not what bounds the kernel and the output keeps the 32-bit
+//     weights' precision.  Over an e4m3 cache P is f16.
 //   * The cache's length is split.  All key tiles of all (sequence, kv head)
 //     pairs form one line that is cut into equal pieces, one per warp, so
 //     ragged lengths cost no balance.  A piece that holds a whole (sequence,
@@ -16,16 +20,20 @@
 //     decode_join_kernel joins the parts: M = max m_j, l = sum l_j 2^(m_j - M),
 //     o = sum O_j 2^(m_j - M) / l.  The order is fixed, so runs repeat bit for
 //     bit.
+//     Pieces go to warps side by side: where the heads allow it, the 2 or 4
+//     warps of a team walk the same keys of adjacent heads, so that the 256
+//     (bf16) or 128 (e4m3) bytes that a head has of a key are read together
+//     with its neighbours' (32/8 heads e4m3, 64 x 8192 keys: 181 us against
+//     203 with heads apart).
 //   * A warp streams its keys through a ring of cp.async stages of its own and
 //     waits for no other warp: the start and the end of one's segment overlap
-//     the other seven's streams on the SM.
-//   * With at most 8 query heads per kv head (SMALL) the product's other 8
-//     rows carry what the rounding of the weights to bf16 leaves out: P = P_hi
-//     + P_lo costs no further product, and rows 8-15 need no exponentials.
+//     the others' streams on the SM.
 // Keys past the end, and keys whose page is not in the cache, are not read:
 // their rows are filled with zeros and masked, so what lies there (NaN too)
 // does not matter.
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "paged.cuh"
 
@@ -33,18 +41,17 @@ namespace zq {
 
 namespace {
 
-constexpr int kDecWarps = 4;
-constexpr int kDecThreads = kDecWarps * 32;
-constexpr int kRows = 16;      // query heads per head tile
-constexpr int kMaxCtas = 320;  // the workspace has room for their pieces
-constexpr int kMaxPieces = kMaxCtas * kDecWarps;
+constexpr int kHeads = 8;        // query heads per product (n8)
+constexpr int kMaxHeads = 16;    // query heads per head tile
 constexpr int kCtasPerSm = 2;
-constexpr int kSlot = kRows * 128 + 2 * kRows;  // floats of a part: O, then (m, l) per row
+constexpr int kMaxEntries = 1280;  // warps that the workspace has room for
 // What a segment costs beyond its tiles (first loads, last stores), in tiles:
-// a piece of many short segments gets fewer of them.
-constexpr int kSegmentCost = 2;
+// a piece of many short segments gets fewer of them (64 sequences of 1 to 4096
+// keys, 32/8 heads bf16: 51 us with 1, 48 with 2, 44 with 4 and with 8).
+constexpr int kSegmentCost = 4;
 constexpr int kJoinWarps = 8;
-constexpr int kJoinAlone = 8;  // parts that one warp joins by itself
+constexpr int kJoinAlone = 24;  // parts that one warp joins by itself
+constexpr unsigned kJoinStep = 733;  // prime, and no divisor of a number of entries (at most 1280)
 
 struct DecodeParams {
   PagedKV c;
@@ -54,26 +61,34 @@ struct DecodeParams {
   float* lse;
   float scale;
   int Hq, group, head_tiles;
+  int team;      // warps that walk the same keys of adjacent heads: 1, 2 or 4, dividing the flat head tiles
+  int slot;      // floats of a part: O of 8 or 16 heads, then their (m, l)
   // workspace: who cuts what, then the parts
-  int4* cut;     // [piece] {sequence, flat head tile, parts, 0} of the segment that this piece begins and does not finish
-  float* part;   // [piece][2][kSlot]: slot 0 a segment begun by an earlier piece, slot 1 one left to later pieces
+  int4* cut;     // [piece][team] {sequence, flat head tile, parts, 0} of the segment that this piece begins and does not finish
+  float* part;   // [piece][team][2][slot]: slot 0 a segment begun by an earlier piece, slot 1 one left to later pieces
 };
 
-template <int DQK, int FP8>
+template <int DQK, int FP8, int NT>
 struct DecGeo {
   static constexpr int DV = 128;
   static constexpr int ES = FP8 ? 1 : 2;
-  static constexpr int KW = FP8 ? 32 : 16;              // keys per tile (one step of a warp)
   static constexpr int KCH = DQK * ES / 16;             // 16-byte pieces per key row
   static constexpr int VCH = DV * ES / 16;
-  static constexpr int KBYTES = KW * KCH * 16;
-  static constexpr int VBYTES = KW * VCH * 16;
+  // keys per tile (one step of a warp): 8 or 10 KB either way
+  static constexpr int KEYS = FP8 ? 32 : 16;
+  static constexpr int KB = KEYS / 16;                  // 16-key blocks of a tile
+  static constexpr int KBYTES = KEYS * KCH * 16;
+  static constexpr int VBYTES = KEYS * VCH * 16;
   static constexpr int STAGE = KBYTES + VBYTES;
-  static constexpr int NS = DQK == 128 ? 3 : 2;         // stages that fit 113 KB (two CTAs per SM)
+  static constexpr unsigned ALL = 0xffffffffu >> (32 - KEYS);
+  static constexpr int WARPS = 4;
+  static constexpr int THREADS = WARPS * 32;
+  static constexpr int FIT = 113 * 1024 / WARPS / STAGE;  // two CTAs per SM
+  static constexpr int NS = FIT < 6 ? FIT : 6;
   static constexpr int RING = NS * STAGE;               // bytes per warp
-  static constexpr int SMEM = kDecWarps * RING;
+  static constexpr int SMEM = WARPS * RING;
   static constexpr int QK_STEPS = DQK / 16;
-  static_assert(SMEM <= 113 * 1024, "two CTAs per SM");
+  static_assert(NS >= 2, "a stage in use and one in flight");
   // place of piece ch of row r: pieces of eight rows fall in different banks
   __device__ static constexpr uint32_t at_k(int r, int ch) {
     return (uint32_t)(r * KCH + (KCH % 8 == 0 ? (ch ^ (r & 7)) : (ch ^ ((r >> 1) & 3)))) * 16;
@@ -81,38 +96,46 @@ struct DecGeo {
   __device__ static constexpr uint32_t at_v(int r, int ch) { return (uint32_t)(r * VCH + (ch ^ (r & 7))) * 16; }
 };
 
+// Transposes an 8 x 8 tile of 16-bit values that the warp holds two a lane.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
 __device__ __forceinline__ int keys_of(const PagedKV& c, int b) {
   const int64_t cap = (int64_t)c.table_width << c.page_shift;
   return (int)min((int64_t)max(c.seqlens[b], 0), cap);
 }
 
-template <int DQK, int FP8, int SMALL>
-__global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const DecodeParams p) {
-  using G = DecGeo<DQK, FP8>;
-  constexpr int DV = G::DV, KW = G::KW, NS = G::NS;
-  constexpr int HF = SMALL ? 1 : 2;  // rows quad, and quad + 8 unless SMALL
+template <int DQK, int FP8, int NT>
+__global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) decode_kernel(const DecodeParams p) {
+  using G = DecGeo<DQK, FP8, NT>;
+  constexpr int DV = G::DV, NS = G::NS, WARPS = G::WARPS, THREADS = G::THREADS;
   constexpr unsigned kFull = 0xffffffffu;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t scan[kDecWarps];
-  __shared__ int64_t first_off[kDecWarps];
-  __shared__ int first_b[kDecWarps];
+  __shared__ int64_t scan[WARPS];
+  __shared__ int64_t first_off[WARPS];
+  __shared__ int first_b[WARPS];
   const PagedKV& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane >> 2, ql = lane & 3;
-  const int heads = c.Hkv * p.head_tiles;
+  const int heads = c.Hkv * p.head_tiles / p.team;  // teams of flat head tiles
   launch_dependents();
 
-  // ---- the line: b outermost, then the flat head tile, then kSegmentCost
+  // ---- the line: b outermost, then the team's heads, then kSegmentCost
   // places without a tile and the key tiles
   auto places = [&](int b) -> int64_t {
     const int n = keys_of(c, b);
-    return n > 0 ? (int64_t)((n + KW - 1) / KW + kSegmentCost) * heads : 0;
+    return n > 0 ? (int64_t)((n + G::KEYS - 1) / G::KEYS + kSegmentCost) * heads : 0;
   };
   int64_t x = 0, x1 = 0, line = 0;  // this warp's piece
   int pieces;
-  const int piece = warp * gridDim.x + blockIdx.x;  // (few pieces are spread over the SMs)
+  const int per_cta = WARPS / p.team;
+  const int piece = warp / p.team * gridDim.x + blockIdx.x;  // (few pieces are spread over the SMs)
+  const int mine_at = piece * p.team + warp % p.team;        // this warp's entry of cut and part
   {
-    const int per = (c.B + kDecThreads - 1) / kDecThreads;
+    const int per = (c.B + THREADS - 1) / THREADS;
     const int b0 = min((int)threadIdx.x * per, c.B), b1 = min(b0 + per, c.B);
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) mine += places(b);
@@ -126,14 +149,14 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
     __syncthreads();
     int64_t before = 0;
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       if (w < warp) before += scan[w];
       line += scan[w];
     }
     // no more pieces than places, so that none is empty
-    pieces = (int)min((int64_t)gridDim.x * kDecWarps, line);
+    pieces = (int)min((int64_t)gridDim.x * per_cta, line);
     const int64_t at0 = before + sum - mine;  // place of this thread's first sequence
-    for (int w = 0; w < kDecWarps; ++w) {
+    for (int w = 0; w < per_cta; ++w) {
       const int pw = w * gridDim.x + blockIdx.x;
       if (pw >= pieces) break;
       const int64_t y = line * pw / pieces;
@@ -157,132 +180,110 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
   // sequences without keys: 0 and -inf
   for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
     if (keys_of(c, b) > 0) continue;
-    for (int i = threadIdx.x; i < p.Hq * DV / 2; i += kDecThreads)
+    for (int i = threadIdx.x; i < p.Hq * DV / 2; i += THREADS)
       reinterpret_cast<uint32_t*>(p.out + (int64_t)b * p.Hq * DV)[i] = 0u;
     if (p.lse)
-      for (int i = threadIdx.x; i < p.Hq; i += kDecThreads) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
+      for (int i = threadIdx.x; i < p.Hq; i += THREADS) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
   }
 
   const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(smem + warp * G::RING));
+  const int64_t krow = (int64_t)c.Hkv * (DQK * G::ES), vrow = (int64_t)c.Hkv * (DV * G::ES);
   int4 cut = make_int4(0, 0, 0, 0);  // the segment of this piece that is left to later ones
 
-  int b = x < x1 ? first_b[warp] : 0;
-  int64_t off = x < x1 ? first_off[warp] : 0;
+  int b = x < x1 ? first_b[warp / p.team] : 0;
+  int64_t off = x < x1 ? first_off[warp / p.team] : 0;
   while (x < x1) {
     const int len = keys_of(c, b);
-    const int tiles = (len + KW - 1) / KW, span = tiles + kSegmentCost;
+    const int tiles = (len + G::KEYS - 1) / G::KEYS, span = tiles + kSegmentCost;
     if (len == 0 || off >= (int64_t)span * heads) {
       off -= len == 0 ? 0 : (int64_t)span * heads;
       ++b;
       continue;
     }
-    const int fh = (int)(off / span), r0 = (int)(off % span);
+    const int fh = (int)(off / span) * p.team + warp % p.team, r0 = (int)(off % span);
     const int r1 = (int)min((int64_t)span, r0 + (x1 - x));
-    const int64_t start = x - r0;  // the (sequence, head)'s first place
+    const int64_t start = x - r0;  // the (sequence, team)'s first place
     x += r1 - r0;
     off += r1 - r0;
     const int t0 = max(r0 - kSegmentCost, 0);
     const int steps = r1 - kSegmentCost - t0;
     if (steps <= 0) continue;
     const int g = fh / p.head_tiles, ht = fh % p.head_tiles;
-    const int h0 = g * p.group + ht * kRows;          // first query head of the tile
-    const int rows = min(kRows, p.group - ht * kRows);  // query heads in it
+    const int h0 = g * p.group + ht * kMaxHeads;            // first query head of the tile
+    const int rows = min(kMaxHeads, p.group - ht * kMaxHeads);  // query heads in it
 
-    // ---- queries as A fragments: rows quad and quad + 8
-    uint32_t qa[G::QK_STEPS][4];
-    if constexpr (SMALL) {
-#pragma unroll
-      for (int ks = 0; ks < G::QK_STEPS; ++ks) qa[ks][1] = qa[ks][3] = 0u;
-    }
-    const float c2 = p.scale * (FP8 && c.k_descale ? c.k_descale[c.descale_per_head ? g : 0] : 1.0f) * 1.4426950408889634f;
-    float cr[2] = {c2, c2};
-    {
-      const __nv_bfloat16* qrow = p.q + b * p.q_stride + (int64_t)h0 * DQK;
-#pragma unroll
-      for (int hf = 0; hf < HF; ++hf) {
-        const int r = quad + hf * 8;
-        const bool there = r < rows;
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(qrow + (int64_t)r * DQK);
-        if constexpr (!FP8) {
-#pragma unroll
-          for (int ks = 0; ks < G::QK_STEPS; ++ks) {
-            qa[ks][hf] = there ? src[ks * 8 + ql] : 0u;
-            qa[ks][2 + hf] = there ? src[ks * 8 + 4 + ql] : 0u;
-          }
-        } else {
-          // f16 operands (an e4m3 value is exact in f16).  A power of two
-          // brings the row's largest query to [1, 2), so the bf16 values fit
-          // f16's range, exactly for all within 2^-14 of the largest; the
-          // factor goes into the score scale.  Element order: a lane's four
-          // bytes of a 16-byte key piece are channels 4 ql .. 4 ql + 3.
-          float big = 0.0f;
-          uint32_t w[G::QK_STEPS][2];
-#pragma unroll
-          for (int ks = 0; ks < G::QK_STEPS; ++ks) {
-            w[ks][0] = there ? src[ks * 8 + 2 * ql] : 0u;
-            w[ks][1] = there ? src[ks * 8 + 2 * ql + 1] : 0u;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[ks][i] << 16)), fabsf(__uint_as_float(w[ks][i] & 0xffff0000u))));
-          }
-          big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
-          big = fmaxf(big, __shfl_xor_sync(kFull, big, 2));
-          const int ex = (int)(__float_as_uint(big) >> 23);  // biased exponent (0: subnormal or zero)
-          const int e = ex == 255 ? 0 : min(max(ex - 127, -126), 126);
-          const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
-          cr[hf] = c2 * __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-          for (int ks = 0; ks < G::QK_STEPS; ++ks)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              qa[ks][2 * i + hf] = pack_f16x2(__uint_as_float(w[ks][i] << 16) * down, __uint_as_float(w[ks][i] & 0xffff0000u) * down);
-        }
-      }
-    }
-
-    // ---- the segment's keys
+    // ---- the segment's keys: tile `step` holds keys key0 + step * 16 ...
     const int32_t* table = c.table + b * c.table_stride;
-    const int key0 = t0 * KW;
+    const int key0 = t0 * G::KEYS;
     const char* kbase = c.k + (int64_t)g * (DQK * G::ES);
     const char* vbase = c.v + (int64_t)g * (DV * G::ES);
-    const int64_t krow = (int64_t)c.Hkv * (DQK * G::ES), vrow = (int64_t)c.Hkv * (DV * G::ES);
     const int page_mask = (1 << c.page_shift) - 1;
-    // the page of key (step, lane), or -1: not there
+    const bool whole = G::KEYS <= page_mask + 1;  // a tile lies in one page
+    // the page of key (step, lane % KEYS), or -1: not there
     auto page_at = [&](int step) -> int {
-      const int key = key0 + step * KW + lane;
+      const int key = key0 + step * G::KEYS + (lane & (G::KEYS - 1));
       int pg = -1;
-      if (lane < KW && step < steps && key < len) pg = table[key >> c.page_shift];
+      if (step < steps && key < len) pg = table[key >> c.page_shift];
       return (unsigned)pg < (unsigned)c.num_pages ? pg : -1;
     };
     unsigned have[NS];  // which keys of each stage are there
     auto load = [&](int step, int s, int pg) {
-      const unsigned vm = __ballot_sync(kFull, pg >= 0);
+      const unsigned vm = __ballot_sync(kFull, pg >= 0) & G::ALL;
 #pragma unroll
       for (int i = 0; i < NS; ++i)
         if (i == s) have[i] = vm;
       const uint32_t sk = ring_u + s * G::STAGE, sv = sk + G::KBYTES;
-      const int kb = key0 + step * KW;
+      const int kb = key0 + step * G::KEYS;
+      if (whole) {
+        // the tile lies in one page: rows at fixed distances.  Where a row is
+        // 8, 16 or 32 pieces, the lane's piece is the same in all of them.
+        const int64_t page = max(__shfl_sync(kFull, pg, 0), 0);  // (a tile's first key is there if any is)
+        const int64_t row = kb & page_mask;
+        const char* ks = kbase + page * c.k_page + row * krow;
+        const char* vs = vbase + page * c.v_page + row * vrow;
+        auto rows_of = [&](auto all) {
+          auto copy = [&](uint32_t dst, const char* src, int r) {
+            if constexpr (all.value)
+              cp_async16(dst, src);
+            else
+              cp_async16(dst, src, (vm >> r) & 1u ? 16 : 0);
+          };
+          if constexpr (32 % G::KCH == 0) {
+            constexpr int R = 32 / G::KCH;
+            const int r0 = lane / G::KCH, ch = lane % G::KCH;
+            const char* src = ks + r0 * krow + ch * 16;
 #pragma unroll
-      for (int i = 0; i < KW * G::KCH / 32; ++i) {
-        const int idx = i * 32 + lane, r = idx / G::KCH, ch = idx % G::KCH;
-        const int rp = __shfl_sync(kFull, pg, r);
-        const char* src = kbase + max(rp, 0) * c.k_page + ((kb + r) & page_mask) * krow + ch * 16;
-        cp_async16(sk + G::at_k(r, ch), src, rp >= 0 ? 16 : 0);
-      }
+            for (int i = 0; i < G::KEYS / R; ++i, src += R * krow) copy(sk + G::at_k(r0 + R * i, ch), src, r0 + R * i);
+          } else {
 #pragma unroll
-      for (int i = 0; i < KW * G::VCH / 32; ++i) {
-        const int idx = i * 32 + lane, r = idx / G::VCH, ch = idx % G::VCH;
-        const int rp = __shfl_sync(kFull, pg, r);
-        const char* src = vbase + max(rp, 0) * c.v_page + ((kb + r) & page_mask) * vrow + ch * 16;
-        cp_async16(sv + G::at_v(r, ch), src, rp >= 0 ? 16 : 0);
+            for (int i = 0; i < G::KEYS * G::KCH / 32; ++i) {
+              const int idx = i * 32 + lane, r = idx / G::KCH, ch = idx % G::KCH;
+              copy(sk + G::at_k(r, ch), ks + r * krow + ch * 16, r);
+            }
+          }
+          constexpr int R = 32 / G::VCH;
+          const int r0 = lane / G::VCH, ch = lane % G::VCH;
+          const char* src = vs + r0 * vrow + ch * 16;
+#pragma unroll
+          for (int i = 0; i < G::KEYS / R; ++i, src += R * vrow) copy(sv + G::at_v(r0 + R * i, ch), src, r0 + R * i);
+        };
+        if (vm == G::ALL)
+          rows_of(std::true_type{});
+        else
+          rows_of(std::false_type{});
+      } else {
+#pragma unroll 1
+        for (int idx = lane; idx < G::KEYS * G::KCH; idx += 32) {
+          const int r = idx / G::KCH, ch = idx % G::KCH, rp = __shfl_sync(kFull, pg, r);
+          cp_async16(sk + G::at_k(r, ch), kbase + max(rp, 0) * c.k_page + ((kb + r) & page_mask) * krow + ch * 16, rp >= 0 ? 16 : 0);
+        }
+#pragma unroll 1
+        for (int idx = lane; idx < G::KEYS * G::VCH; idx += 32) {
+          const int r = idx / G::VCH, ch = idx % G::VCH, rp = __shfl_sync(kFull, pg, r);
+          cp_async16(sv + G::at_v(r, ch), vbase + max(rp, 0) * c.v_page + ((kb + r) & page_mask) * vrow + ch * 16, rp >= 0 ? 16 : 0);
+        }
       }
     };
-
-    float o[DV / 8][4];
-#pragma unroll
-    for (int n = 0; n < DV / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
-    float ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-
     int pg = page_at(0);
 #pragma unroll
     for (int s = 0; s < NS - 1; ++s) {
@@ -290,6 +291,70 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
       cp_async_commit();
       pg = page_at(s + 1);
     }
+
+    // ---- queries as B fragments: column (head) quad of each product, and the
+    // score scale of the columns 2 ql, 2 ql + 1 that this lane holds of S^T
+    uint32_t qb[NT][G::QK_STEPS][2];
+    const float c2 = p.scale * (FP8 && c.k_descale ? c.k_descale[c.descale_per_head ? g : 0] : 1.0f) * 1.4426950408889634f;
+    float cr[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = nt * kHeads + quad;
+      const bool there = h < rows;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + b * p.q_stride + (int64_t)(h0 + (there ? h : 0)) * DQK);
+      if constexpr (!FP8) {
+#pragma unroll
+        for (int ks = 0; ks < G::QK_STEPS; ++ks) {
+          qb[nt][ks][0] = there ? src[ks * 8 + ql] : 0u;
+          qb[nt][ks][1] = there ? src[ks * 8 + 4 + ql] : 0u;
+        }
+        cr[nt][0] = cr[nt][1] = c2;
+      } else {
+        // f16 operands (an e4m3 value is exact in f16).  A power of two brings
+        // the head's largest query to [1, 2), so the bf16 values fit f16's
+        // range, exactly for all within 2^-14 of the largest; the factor goes
+        // into the score scale.  Order: a lane's four bytes of a 16-byte key
+        // piece are channels 4 ql .. 4 ql + 3.
+        float big = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < G::QK_STEPS; ++ks)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w = there ? src[ks * 8 + 2 * ql + i] : 0u;
+            qb[nt][ks][i] = w;
+            big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))));
+          }
+        big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(kFull, big, 2));
+        const int ex = (int)(__float_as_uint(big) >> 23);  // biased exponent (0: subnormal or zero)
+        const int e = ex == 255 ? 0 : min(max(ex - 127, -126), 126);
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
+#pragma unroll
+        for (int ks = 0; ks < G::QK_STEPS; ++ks) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w = qb[nt][ks][i];
+            qb[nt][ks][i] = pack_f16x2(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down);
+          }
+        }
+        const float mine = c2 * __uint_as_float((uint32_t)(127 + e) << 23);
+        cr[nt][0] = __shfl_sync(kFull, mine, ql * 8);
+        cr[nt][1] = __shfl_sync(kFull, mine, ql * 8 + 4);
+      }
+    }
+
+    // O^T: rows (channels) by heads.  bf16: row quad, quad + 8 of 16 i are
+    // channels 16 i + quad, + 8; e4m3: 16 i + 2 quad, + 1.
+    float o[NT][DV / 16][4];
+    float ref[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < DV / 16; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
+      ref[nt][0] = ref[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.0f;
+    }
+
     for (int st0 = 0; st0 < steps; st0 += NS) {
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
@@ -304,98 +369,129 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
         __syncwarp();
         const uint32_t sk = ring_u + s * G::STAGE, sv = sk + G::KBYTES;
 
-        // S = Q K^T
-        float sc[KW / 8][4];
+        // S^T = K Q^T: of each 16 keys the lane holds quad (i < 2) and quad + 8 of heads 2 ql + (i & 1)
+        float sc[NT][G::KB][4];
 #pragma unroll
-        for (int n = 0; n < KW / 8; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int ks = 0; ks < G::QK_STEPS; ++ks) {
-          uint32_t kf[4];
-          if constexpr (!FP8) {
-            const int r = ((lane >> 4) << 3) + (lane & 7), ch = 2 * ks + ((lane >> 3) & 1);
-            ldmatrix_x4(kf, sk + G::at_k(r, ch));
-            mma_16816<false>(sc[0], qa[ks], kf[0], kf[1]);
-            mma_16816<false>(sc[1], qa[ks], kf[2], kf[3]);
-          } else {
-            ldmatrix_x4(kf, sk + G::at_k(lane, ks));
+          for (int kb = 0; kb < G::KB; ++kb) sc[nt][kb][0] = sc[nt][kb][1] = sc[nt][kb][2] = sc[nt][kb][3] = 0.0f;
+        if constexpr (!FP8) {
+          const int mr = (lane & 7) + ((lane >> 3) & 1) * 8, mc = lane >> 4;
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-              mma_16816<true>(sc[n], qa[ks], e4m3x2_to_f16x2(kf[n]), e4m3x2_to_f16x2(kf[n] >> 16));
+          for (int ks = 0; ks < G::QK_STEPS; ++ks) {
+            uint32_t a[4];
+            ldmatrix_x4(a, sk + G::at_k(mr, 2 * ks + mc));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_16816<false>(sc[nt][0], a, qb[nt][ks][0], qb[nt][ks][1]);
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < G::QK_STEPS; ++ks) {
+            uint32_t w[4], a[4];
+            ldmatrix_x4(w, sk + G::at_k(lane, ks));
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+              e4m3x4_to_f16x4(w[2 * kb], a[0], a[2]);
+              e4m3x4_to_f16x4(w[2 * kb + 1], a[1], a[3]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_16816<true>(sc[nt][kb], a, qb[nt][ks][0], qb[nt][ks][1]);
+            }
           }
         }
         // log2 domain, mask
         const unsigned vm = have[s];
-        float mx[HF];
+        float mx[NT][2];
+        bool move = false;
 #pragma unroll
-        for (int hf = 0; hf < HF; ++hf) {
-          mx[hf] = -INFINITY;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int n = 0; n < KW / 8; ++n)
+          for (int kb = 0; kb < G::KB; ++kb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[nt][kb][i] *= cr[nt][i & 1];
+        if (vm != G::ALL) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int kb = 0; kb < G::KB; ++kb)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (!((vm >> (kb * 16 + quad + (i >> 1) * 8)) & 1u)) sc[nt][kb][i] = -INFINITY;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mx[nt][i] = fmaxf(sc[nt][0][i], sc[nt][0][2 + i]);
+            if constexpr (G::KB == 2) mx[nt][i] = fmaxf(mx[nt][i], fmaxf(sc[nt][1][i], sc[nt][1][2 + i]));
+            move |= mx[nt][i] > ref[nt][i] + 8.0f;
+          }
+        // the reference moves when a score passes it by 8 (weights stay below 2^8)
+        if (__any_sync(kFull, move)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float& z = sc[n][2 * hf + i];
-              z *= cr[hf];
-              if (!((vm >> (n * 8 + 2 * ql + i)) & 1u)) z = -INFINITY;
-              mx[hf] = fmaxf(mx[hf], z);
+              float m = mx[nt][i];
+              m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
+              m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
+              m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
+              const float nref = fmaxf(ref[nt][i], m);
+              const float f = (nref == -INFINITY || nref == ref[nt][i]) ? 1.0f : ex2_approx(ref[nt][i] - nref);
+              ref[nt][i] = nref;
+              l[nt][i] *= f;
+#pragma unroll
+              for (int n = 0; n < DV / 16; ++n) {
+                o[nt][n][i] *= f;
+                o[nt][n][2 + i] *= f;
+              }
             }
         }
-        // the reference moves when a score passes it by 8 (weights stay below 2^8)
-        if (__any_sync(kFull, mx[0] > ref[0] + 8.0f || mx[HF - 1] > ref[HF - 1] + 8.0f)) {
-          float f[2];
+        uint32_t pb[NT][G::KB][2], pl[NT][2];  // P^T as B fragments: keys 2 ql, 2 ql + 1 (and + 8) of head quad
 #pragma unroll
-          for (int hf = 0; hf < HF; ++hf) {
-            float m = fmaxf(mx[hf], __shfl_xor_sync(kFull, mx[hf], 1));
-            m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-            const float nref = fmaxf(ref[hf], m);
-            f[hf] = (nref == -INFINITY || nref == ref[hf]) ? 1.0f : ex2_approx(ref[hf] - nref);
-            ref[hf] = nref;
-            l[hf] *= f[hf];
-          }
-          if (SMALL) f[1] = f[0];  // the low parts of the same heads
+        for (int nt = 0; nt < NT; ++nt) {
+          const float n0 = ref[nt][0] == -INFINITY ? 0.0f : ref[nt][0], n1 = ref[nt][1] == -INFINITY ? 0.0f : ref[nt][1];
 #pragma unroll
-          for (int n = 0; n < DV / 8; ++n)
+          for (int kb = 0; kb < G::KB; ++kb)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][i] *= f[i >> 1];
+            for (int kh = 0; kh < 2; ++kh) {
+              const float p0 = ex2_approx(sc[nt][kb][2 * kh] - n0), p1 = ex2_approx(sc[nt][kb][2 * kh + 1] - n1);
+              l[nt][0] += p0;
+              l[nt][1] += p1;
+              if constexpr (FP8) {
+                pb[nt][kb][kh] = transpose_8x8(pack_f16x2(p0, p1));
+              } else {
+                const uint32_t w = pack_bf16x2(p0, p1);
+                pb[nt][kb][kh] = transpose_8x8(w);
+                pl[nt][kh] = transpose_8x8(pack_bf16x2(p0 - __uint_as_float(w << 16), p1 - __uint_as_float(w & 0xffff0000u)));
+              }
+            }
         }
-        uint32_t pa[KW / 16][4];
-#pragma unroll
-        for (int hf = 0; hf < HF; ++hf) {
-          const float nb = ref[hf] == -INFINITY ? 0.0f : ref[hf];
-#pragma unroll
-          for (int n = 0; n < KW / 8; ++n) {
-            const float p0 = ex2_approx(sc[n][2 * hf] - nb), p1 = ex2_approx(sc[n][2 * hf + 1] - nb);
-            l[hf] += p0 + p1;
-            const uint32_t w = FP8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-            pa[n / 2][(n & 1) * 2 + hf] = w;
-            if constexpr (SMALL && !FP8)
-              pa[n / 2][(n & 1) * 2 + 1] = pack_bf16x2(p0 - __uint_as_float(w << 16), p1 - __uint_as_float(w & 0xffff0000u));
-            else if constexpr (SMALL)
-              pa[n / 2][(n & 1) * 2 + 1] = 0u;
-          }
-        }
-        // O += P V
+        // O^T += V^T P^T
         if constexpr (!FP8) {
+          const int vr = (lane & 7) + (lane >> 4) * 8, vc = (lane >> 3) & 1;
 #pragma unroll
-          for (int cp = 0; cp < G::VCH / 2; ++cp) {
-            uint32_t vf[4];
-            const int r = ((lane >> 3) & 1) * 8 + (lane & 7), ch = 2 * cp + (lane >> 4);
-            ldmatrix_x4_trans(vf, sv + G::at_v(r, ch));
-            mma_16816<false>(o[2 * cp], pa[0], vf[0], vf[1]);
-            mma_16816<false>(o[2 * cp + 1], pa[0], vf[2], vf[3]);
+          for (int i = 0; i < DV / 16; ++i) {
+            uint32_t a[4];
+            ldmatrix_x4_trans(a, sv + G::at_v(vr, 2 * i + vc));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_16816<false>(o[nt][i], a, pb[nt][0][0], pb[nt][0][1]);
+              mma_16816<false>(o[nt][i], a, pl[nt][0], pl[nt][1]);
+            }
           }
         } else {
           // a 16-bit element of the transposed load is two channels of a key:
-          // the even ones go to product 2 ch, the odd ones to 2 ch + 1
+          // the even ones are rows quad, the odd ones rows quad + 8
 #pragma unroll
-          for (int ch = 0; ch < G::VCH; ++ch) {
-            uint32_t vf[4];
-            ldmatrix_x4_trans(vf, sv + G::at_v(lane, ch));
+          for (int i = 0; i < DV / 16; ++i) {
+            uint32_t w[4], a[4];
+            ldmatrix_x4_trans(w, sv + G::at_v(lane, i));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) vf[i] = prmt(vf[i], 0u, 0x3120u);
+            for (int kb = 0; kb < 2; ++kb) {
+              e4m3x4_to_f16x4(prmt(w[2 * kb], 0u, 0x3120u), a[0], a[1]);
+              e4m3x4_to_f16x4(prmt(w[2 * kb + 1], 0u, 0x3120u), a[2], a[3]);
 #pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2) {
-              mma_16816<true>(o[2 * ch], pa[k2], e4m3x2_to_f16x2(vf[2 * k2]), e4m3x2_to_f16x2(vf[2 * k2 + 1]));
-              mma_16816<true>(o[2 * ch + 1], pa[k2], e4m3x2_to_f16x2(vf[2 * k2] >> 16), e4m3x2_to_f16x2(vf[2 * k2 + 1] >> 16));
+              for (int nt = 0; nt < NT; ++nt) mma_16816<true>(o[nt][i], a, pb[nt][kb][0], pb[nt][kb][1]);
             }
           }
         }
@@ -404,54 +500,53 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
     cp_async_wait<0>();
     __syncwarp();
 
-    // ---- the segment's end: to the output, or to this piece's slot
+    // ---- the segment's end: to the output, or to this piece's slot.  O^T goes
+    // through the ring so that rows of channels are written whole.
     const bool begins = t0 == 0, ends = t0 + steps == tiles;
     const float vds = FP8 && c.v_descale ? c.v_descale[c.descale_per_head ? g : 0] : 1.0f;
-    float* const slot = p.part + ((int64_t)piece * 2 + (begins ? 1 : 0)) * kSlot;
+    float* const slot = p.part + ((int64_t)mine_at * 2 + (begins ? 1 : 0)) * p.slot;
+    float* const turn = reinterpret_cast<float*>(smem + warp * G::RING);  // [8 heads][132]
+    constexpr int PITCH = DV + 4;
+    static_assert(kHeads * PITCH * 4 <= G::RING, "a product's O fits the ring");
 #pragma unroll
-    for (int hf = 0; hf < HF; ++hf) {
-      l[hf] += __shfl_xor_sync(kFull, l[hf], 1);
-      l[hf] += __shfl_xor_sync(kFull, l[hf], 2);
-      if (SMALL && !FP8) {
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int n = 0; n < DV / 8; ++n) {
-          o[n][0] += o[n][2];
-          o[n][1] += o[n][3];
+      for (int i = 0; i < 2; ++i) {
+        l[nt][i] += __shfl_xor_sync(kFull, l[nt][i], 4);
+        l[nt][i] += __shfl_xor_sync(kFull, l[nt][i], 8);
+        l[nt][i] += __shfl_xor_sync(kFull, l[nt][i], 16);
+#pragma unroll
+        for (int n = 0; n < DV / 16; ++n) {
+          float* dst = turn + (2 * ql + i) * PITCH + n * 16;
+          if constexpr (!FP8) {
+            dst[quad] = o[nt][n][i];
+            dst[quad + 8] = o[nt][n][2 + i];
+          } else {
+            *reinterpret_cast<float2*>(dst + 2 * quad) = make_float2(o[nt][n][i], o[nt][n][2 + i]);
+          }
         }
       }
-      const int r = quad + hf * 8;
-      if (r >= rows) continue;
-      if (begins && ends) {
-        const int64_t row = (int64_t)b * p.Hq + h0 + r;
-        // no key was there (l = 0): 0 and -inf; NaN stays NaN
-        const bool empty = l[hf] == 0.0f;
-        const float inv = vds / l[hf];
-        auto two = [&](float a, float z) { return empty ? 0u : pack_bf16x2(a * inv, z * inv); };
-        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * DV);
-        if constexpr (!FP8) {
+      __syncwarp();
 #pragma unroll
-          for (int n = 0; n < DV / 8; ++n) dst[n * 4 + ql] = two(o[n][2 * hf], o[n][2 * hf + 1]);
+      for (int r = 0; r < kHeads; ++r) {
+        const int h = nt * kHeads + r;
+        const float m = __shfl_sync(kFull, ref[nt][r & 1], r >> 1), sum = __shfl_sync(kFull, l[nt][r & 1], r >> 1);
+        if (h >= rows) break;
+        const float4 v = *reinterpret_cast<const float4*>(turn + r * PITCH + lane * 4);
+        if (begins && ends) {
+          const int64_t row = (int64_t)b * p.Hq + h0 + h;
+          // no key was there (sum = 0): 0 and -inf; NaN stays NaN
+          const bool empty = sum == 0.0f;
+          const float inv = vds / sum;
+          reinterpret_cast<uint2*>(p.out + row * DV)[lane] =
+              empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+          if (p.lse && lane == 0) p.lse[row] = empty ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
         } else {
-#pragma unroll
-          for (int ch = 0; ch < DV / 16; ++ch)
-            reinterpret_cast<uint2*>(dst)[ch * 4 + ql] =
-                make_uint2(two(o[2 * ch][2 * hf], o[2 * ch + 1][2 * hf]), two(o[2 * ch][2 * hf + 1], o[2 * ch + 1][2 * hf + 1]));
+          reinterpret_cast<float4*>(slot + h * DV)[lane] = v;
+          if (lane == 0) *reinterpret_cast<float2*>(slot + p.slot - NT * kHeads * 2 + 2 * h) = make_float2(m, sum);
         }
-        if (p.lse && ql == 0) p.lse[row] = empty ? -INFINITY : (ref[hf] + log2f(l[hf])) * 0.6931471805599453f;
-      } else {
-        float* dst = slot + r * DV;
-        if constexpr (!FP8) {
-#pragma unroll
-          for (int n = 0; n < DV / 8; ++n)
-            *reinterpret_cast<float2*>(dst + n * 8 + 2 * ql) = make_float2(o[n][2 * hf], o[n][2 * hf + 1]);
-        } else {
-#pragma unroll
-          for (int ch = 0; ch < DV / 16; ++ch)
-            *reinterpret_cast<float4*>(dst + ch * 16 + 4 * ql) =
-                make_float4(o[2 * ch][2 * hf], o[2 * ch + 1][2 * hf], o[2 * ch][2 * hf + 1], o[2 * ch + 1][2 * hf + 1]);
-        }
-        if (ql == 0) *reinterpret_cast<float2*>(slot + kRows * DV + 2 * r) = make_float2(ref[hf], l[hf]);
       }
+      __syncwarp();
     }
     if (begins && !ends) {
       // its parts: this piece's and those up to the one of its last place.
@@ -459,9 +554,8 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm) decode_kernel(const D
       const int64_t j = ((start + span) * pieces - 1) / line;
       cut = make_int4(b, fh, (int)(j - piece) + 1, 0);
     }
-    __syncwarp();
   }
-  if (lane == 0) p.cut[piece] = cut;
+  if (lane == 0) p.cut[mine_at] = cut;
 }
 
 // Running (m, l, O) of a row, a lane's four channels of O.
@@ -481,22 +575,53 @@ struct Part {
 };
 
 // Joins the parts of the segments that were cut; blockIdx.y is the query head
-// in the head tile.  A warp joins the few parts of its own piece's segment
+// in the head tile.  A warp joins the few parts of its own entry's segment
 // alone; the parts of a segment with many are shared by the block's warps.
-__global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const DecodeParams p, int pieces) {
+// Entries are dealt to the blocks in an order that is not theirs (a multiple
+// modulo their number), because those of a team, or of equally long sequences,
+// are cut at regular distances.
+__global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const DecodeParams p, int entries) {
   constexpr int DV = 128;
+  constexpr unsigned kFull = 0xffffffffu;
   __shared__ float4 acc_s[kJoinWarps][32];
   __shared__ float2 stat_s[kJoinWarps];
   __shared__ int4 cut_s[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y;
-  const int mine = blockIdx.x * kJoinWarps + warp;
+  auto entry = [&](int w) { return (int)(((blockIdx.x * kJoinWarps + w) * kJoinStep) % (gridDim.x * kJoinWarps)); };
+  const int mine = entry(warp);
+  const int stats = p.slot / (DV + 2) * DV;  // where a part's (m, l) begin
   wait_previous_kernel();
-  // slot 1 of the piece that begins the segment, slot 0 of those after it
-  auto read = [&](Part& t, int piece, int first, int step, int parts) {
-#pragma unroll 4
-    for (int j = first; j < parts; j += step) {
-      const float* s = p.part + ((int64_t)(piece + j) * 2 + (j == 0 ? 1 : 0)) * kSlot;
-      t.add(*reinterpret_cast<const float2*>(s + kRows * DV + 2 * r), reinterpret_cast<const float4*>(s + r * DV)[lane]);
+  // parts first, first + step, ...: 32 at a time, a lane each for (m, l), then
+  // their O with weights that no longer depend on one another.  Slot 1 of the
+  // entry that begins the segment, slot 0 of the same head's in later pieces.
+  auto read = [&](Part& t, int at, int first, int step, int parts) {
+    auto part = [&](int j) { return p.part + ((int64_t)(at + j * p.team) * 2 + (j == 0 ? 1 : 0)) * p.slot; };
+    for (int j0 = first; j0 < parts; j0 += 32 * step) {
+      const int j = j0 + lane * step;
+      const float2 st = j < parts ? *reinterpret_cast<const float2*>(part(j) + stats + 2 * r) : make_float2(-INFINITY, 0.0f);
+      float m = st.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      const float f = ex2_approx(st.x - (m == -INFINITY ? 0.0f : m));
+      float l = st.y * f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
+      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const int n = min((parts - j0 + step - 1) / step, 32);
+      for (int i0 = 0; i0 < n; i0 += 8) {  // eight loads at once; the weights past the last are 0
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = reinterpret_cast<const float4*>(part(j0 + min(i0 + i, n - 1) * step) + r * DV)[lane];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float fi = i0 + i < n ? __shfl_sync(kFull, f, i0 + i) : 0.0f;
+          a.x += v[i].x * fi;
+          a.y += v[i].y * fi;
+          a.z += v[i].z * fi;
+          a.w += v[i].w * fi;
+        }
+      }
+      t.add(make_float2(m, l), a);
     }
   };
   auto write = [&](const Part& t, int4 d) {
@@ -504,13 +629,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Deco
     const bool empty = t.l == 0.0f;
     const float vds = p.c.dtype == 1 && p.c.v_descale ? p.c.v_descale[p.c.descale_per_head ? g : 0] : 1.0f;
     const float inv = vds / t.l;
-    const int64_t row = (int64_t)d.x * p.Hq + g * p.group + ht * kRows + r;
+    const int64_t row = (int64_t)d.x * p.Hq + g * p.group + ht * kMaxHeads + r;
     reinterpret_cast<uint2*>(p.out + row * DV)[lane] =
         empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(t.a.x * inv, t.a.y * inv), pack_bf16x2(t.a.z * inv, t.a.w * inv));
     if (p.lse && lane == 0) p.lse[row] = empty ? -INFINITY : (t.m + log2f(t.l)) * 0.6931471805599453f;
   };
-  int4 d = mine < pieces ? p.cut[mine] : make_int4(0, 0, 0, 0);
-  if (r >= min(kRows, p.group - (d.y % p.head_tiles) * kRows)) d.z = 0;
+  int4 d = mine < entries ? p.cut[mine] : make_int4(0, 0, 0, 0);
+  if (r >= min(kMaxHeads, p.group - (d.y % p.head_tiles) * kMaxHeads)) d.z = 0;
   if (d.z > 0 && d.z <= kJoinAlone) {
     Part t;
     read(t, mine, 0, 1, d.z);
@@ -522,7 +647,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Deco
     const int4 e = cut_s[w];
     if (e.z <= kJoinAlone) continue;
     Part t;
-    read(t, blockIdx.x * kJoinWarps + w, warp, kJoinWarps, e.z);
+    read(t, entry(w), warp, kJoinWarps, e.z);
     acc_s[warp][lane] = t.a;
     if (lane == 0) stat_s[warp] = make_float2(t.m, t.l);
     __syncthreads();
@@ -536,26 +661,42 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Deco
   }
 }
 
-template <int DQK, int FP8, int SMALL>
-cudaError_t launch_kernel(const DecodeParams& p, cudaStream_t st, int grid) {
-  using G = DecGeo<DQK, FP8>;
-  auto kern = decode_kernel<DQK, FP8, SMALL>;
+template <int DQK, int FP8, int NT>
+cudaError_t launch_kernel(DecodeParams& p, cudaStream_t st, int num_sms) {
+  using G = DecGeo<DQK, FP8, NT>;
+  p.slot = NT * kHeads * (G::DV + 2);
+  // one piece per warp of the CTAs that are resident at once
+  constexpr int most = kMaxEntries / G::WARPS;
+  const int grid = num_sms * kCtasPerSm < most ? num_sms * kCtasPerSm : most;
+  auto kern = decode_kernel<DQK, FP8, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kDecThreads, G::SMEM, st>>>(p);
-  return cudaGetLastError();
+  kern<<<grid, G::THREADS, G::SMEM, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int entries = grid * G::WARPS;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((entries + kJoinWarps - 1) / kJoinWarps), (unsigned)(p.group < kMaxHeads ? p.group : kMaxHeads));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel, (const DecodeParams)p, entries);
 }
 
 template <int DQK, int FP8>
-cudaError_t launch_variant(const DecodeParams& p, cudaStream_t st, int grid) {
-  return p.group <= 8 ? launch_kernel<DQK, FP8, 1>(p, st, grid) : launch_kernel<DQK, FP8, 0>(p, st, grid);
+cudaError_t launch_variant(DecodeParams& p, cudaStream_t st, int num_sms) {
+  return p.group <= kHeads ? launch_kernel<DQK, FP8, 1>(p, st, num_sms) : launch_kernel<DQK, FP8, 2>(p, st, num_sms);
 }
 
-constexpr size_t kCutBytes = (size_t)kMaxPieces * 16;
+constexpr size_t kCutBytes = (size_t)kMaxEntries * 16;
 
 }  // namespace
 
-size_t decode_workspace_bytes() { return kCutBytes + (size_t)kMaxPieces * 2 * kSlot * 4; }
+size_t decode_workspace_bytes() { return kCutBytes + (size_t)kMaxEntries * 2 * kMaxHeads * (128 + 2) * 4; }
 
 cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t st, int num_sms) {
   DecodeParams p;
@@ -567,27 +708,13 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t st, int num_sms) {
   p.scale = a.softmax_scale;
   p.Hq = a.Hq;
   p.group = a.Hq / a.c.Hkv;
-  p.head_tiles = (p.group + kRows - 1) / kRows;
+  p.head_tiles = (p.group + kMaxHeads - 1) / kMaxHeads;
+  const int heads = a.c.Hkv * p.head_tiles;
+  p.team = heads % 4 == 0 ? 4 : heads % 2 == 0 ? 2 : 1;
   p.cut = static_cast<int4*>(a.workspace);
   p.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kCutBytes);
-  const int grid = num_sms * kCtasPerSm < kMaxCtas ? num_sms * kCtasPerSm : kMaxCtas;
-  cudaError_t e;
-  if (a.c.dtype == 1)
-    e = a.c.dqk == 128 ? launch_variant<128, 1>(p, st, grid) : launch_variant<192, 1>(p, st, grid);
-  else
-    e = a.c.dqk == 128 ? launch_variant<128, 0>(p, st, grid) : launch_variant<192, 0>(p, st, grid);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  const int pieces = grid * kDecWarps;
-  cfg.gridDim = dim3((unsigned)((pieces + kJoinWarps - 1) / kJoinWarps), (unsigned)(p.group < kRows ? p.group : kRows));
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel, p, pieces);
+  if (a.c.dtype == 1) return a.c.dqk == 128 ? launch_variant<128, 1>(p, st, num_sms) : launch_variant<192, 1>(p, st, num_sms);
+  return a.c.dqk == 128 ? launch_variant<128, 0>(p, st, num_sms) : launch_variant<192, 0>(p, st, num_sms);
 }
 
 }  // namespace zq
