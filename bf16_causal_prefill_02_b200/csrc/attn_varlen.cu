@@ -7,16 +7,10 @@
 // of attn_fwd.cu (same P, same FP8 modes, key blocks counted from the
 // sequence's first key); what differs is the way to it:
 //
-//   * The offsets are read on the device, so the host knows only a bound on
-//     the number of 128-row query tiles: (Tq + 127 B) / 128.  The grid is
-//     that bound times Hq, one CTA per SM is resident, and a CTA that is done
-//     with its unit takes the next not yet started one from the grid
-//     (clusterlaunchcontrol.try_cancel).  Ragged lengths need no schedule on
-//     the host and no counter in memory, and the next unit's loads overlap the
-//     last one's tail.
-//   * A scheduler warp turns a unit's number into (sequence, query tile, head)
-//     with prefix sums of the tile counts and hands it to the other roles
-//     through a two-slot ring.
+//   * The offsets are read on the device, so the host launches a bound on the
+//     work, and resident CTAs take over blocks that have not started
+//     (varlen_sched.cuh).  Ragged lengths need no schedule on the host and no
+//     counter in memory, and a unit's loads overlap the last one's tail.
 //   * Units run in groups of heads that share the L2, inside a group sequence
 //     by sequence, each sequence's longest tiles first.
 //   * The last key tile of a sequence ends in rows of the next one, or in rows
@@ -33,10 +27,12 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "attn_math.cuh"
 #include "schedule.h"
 #include "sm100_ptx.cuh"
+#include "varlen_sched.cuh"
 #include "zq_internal.h"
 
 namespace zq {
@@ -48,7 +44,9 @@ constexpr int kVarThreads = kSmThreads + 96;
 constexpr int kProducer = 8, kIssuer = 9, kScheduler = 10;
 constexpr uint32_t kS0 = 0, kO = 256, kRS = 384, kSFA = 400, kSFB = 408;
 constexpr uint32_t kCols = 512;
-constexpr int kChunks = 256;  // prefix sums of the tile counts, one per chunk of sequences
+// Degree of the software exp2: 4 (2.7e-6) measured the same as the 3 (7.5e-5)
+// of the fixed-batch kernel and keeps the lse of short rows to fp32.
+constexpr int kPolyDegree = 4;
 
 template <int DT, int DQK>
 struct VGeo {
@@ -71,7 +69,7 @@ struct VGeo {
   static constexpr int ONES_BYTES = DT == 1 ? 16384 : 0;
   static constexpr int OFF_SF = OFF_ONES + ONES_BYTES;   // FP8: [2 buf] 512 B scale tiles
   static constexpr int OFF_PREFIX = OFF_SF + (DT == 1 ? 1024 : 0);
-  static constexpr int OFF_UNIT = OFF_PREFIX + kChunks * 4;
+  static constexpr int OFF_UNIT = OFF_PREFIX + kSchedChunks * 4;
   static constexpr int OFF_CLC = OFF_UNIT + 2 * 32;
   static constexpr int OFF_BAR = OFF_CLC + 16;
   static constexpr int NBAR = 4 * NS + 15;
@@ -87,34 +85,6 @@ struct VUnit {
   int lim0;          // last key its first row may see (before the clamp to len_k - 1)
   int n_kv;          // key tiles to visit; -1: no more units
 };
-
-__device__ __forceinline__ void clc_try_cancel(void* response, uint64_t* bar) {
-  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                   smem_u32(response)),
-               "r"(smem_u32(bar))
-               : "memory");
-}
-// The block index that the request took over, or -1: no block is left.
-__device__ __forceinline__ int64_t clc_taken(const void* response) {
-  uint32_t ok, x;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
-      "ld.shared.b128 h, [%2];\n\t"
-      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
-      : "=r"(ok), "=r"(x)
-      : "r"(smem_u32(response))
-      : "memory");
-  return ok ? (int64_t)x : -1;
-}
-
-__device__ __forceinline__ int offset_at(const int32_t* cu, int b, int total) { return min(max(cu[b], 0), total); }
-// query tiles of sequence b (0 for offsets that descend)
-__device__ __forceinline__ int tiles_of(const VarlenParams& p, int b) {
-  const int n = offset_at(p.cu_q, b + 1, p.Tq) - offset_at(p.cu_q, b, p.Tq);
-  return n > 0 ? (n + kTile - 1) / kTile : 0;
-}
 
 template <int DT, int DQK, int MODE, int BS>
 __global__ void __launch_bounds__(kVarThreads, 1)
@@ -140,7 +110,8 @@ __global__ void __launch_bounds__(kVarThreads, 1)
   uint64_t* bar_ofinal = bar_qfree + 1;     // last PV of a unit done
   uint64_t* bar_ofree = bar_ofinal + 1;     // softmax read O of a unit
   uint64_t* bar_clc = bar_ofree + 1;        // the answer to a request for a block
-  uint64_t* bar_drain = bar_clc + 1;        // after an abort: the issuer's work landed
+  uint64_t* bar_want = bar_clc + 1;         // the producer issued a unit's last load
+  uint64_t* bar_drain = bar_want + 1;       // after an abort: the issuer's work landed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + G::NBAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   VUnit* units = reinterpret_cast<VUnit*>(smem + G::OFF_UNIT);
@@ -163,6 +134,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     mbar_init(bar_ofinal, 1);
     mbar_init(bar_ofree, kSmThreads);
     mbar_init(bar_clc, 1);
+    mbar_init(bar_want, 1);
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -172,6 +144,8 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     for (int i = threadIdx.x; i < G::ONES_BYTES / 4; i += kVarThreads) ones[i] = 0x38383838u;
     fence_proxy_async_smem();
   }
+  UnitCount count;  // (the scheduler's; beside the set-up of the others)
+  if (warp == kScheduler) count = count_tiles<kTile>(p, prefix, lane);
   if (warp == kIssuer) {
     tmem_alloc(tmem_slot, kCols);
     tmem_relinquish();
@@ -203,102 +177,24 @@ __global__ void __launch_bounds__(kVarThreads, 1)
 
   if (warp == kScheduler) {
     // ----------------------------------------------------------- scheduler
-    // inclusive prefix sums of the query tiles over chunks of `per` sequences
-    const int per = (p.B + kChunks - 1) / kChunks;
-    const int n_chunks = (p.B + per - 1) / per;
-    int64_t total = 0;  // (offsets that are no ascending sequence may add up to anything: cut at the grid's bound)
-    for (int c0 = 0; c0 < n_chunks; c0 += 32) {
-      const int b0 = (c0 + lane) * per, b1 = min(b0 + per, p.B);
-      int64_t n = 0;
-      for (int b = b0; b < b1; ++b) n += tiles_of(p, b);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(kFull, n, o);
-        if (lane >= o) n += up;
-      }
-      if (c0 + lane < n_chunks) prefix[c0 + lane] = (int)min(total + n, (int64_t)p.max_tiles);
-      total += __shfl_sync(kFull, n, 31);
-    }
-    __syncwarp();
-    const int tiles = (int)min(total, (int64_t)p.max_tiles);
-    const int64_t n_units = (int64_t)tiles * p.Hq;
-    const int GH = p.head_group;
-    bool ok = true, last = false;
-    int64_t u = blockIdx.x;
-    for (int k = 0; ok; ++k) {
-      // a block past the last unit is nobody's: ask on until none is left
-      while (!last && u >= n_units) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar_clc, 16);
-          clc_try_cancel(clc, bar_clc);
-        }
-        asked = true;
-        if (!__all_sync(kFull, mbar_wait(bar_clc, clc_n & 1, lim, abort_flag))) { ok = false; break; }
-        asked = false;
-        ++clc_n;
-        u = clc_taken(clc);
-        fence_proxy_async_smem();
-        __syncwarp();
-        last = u < 0;
-      }
-      if (!ok) break;
-      VUnit w = {};
-      w.n_kv = -1;
-      if (!last) {
-        const int gi = (int)u / (GH * tiles), gr = (int)u % (GH * tiles);  // (units fit 31 bits)
-        const int e = gr / GH;
-        w.h = gi * GH + gr % GH;
-        // the chunk, then the sequence, that holds tile e
-        int ch = 0;
-        for (int c0 = 0; c0 < n_chunks; c0 += 32) {
-          const unsigned le = __ballot_sync(kFull, c0 + lane < n_chunks && prefix[c0 + lane] <= e);
-          ch += __popc(le);
-          if (le != kFull) break;
-        }
-        int r = e - (ch > 0 ? prefix[ch - 1] : 0);  // tile in the chunk
-        int nt = 0;
-        for (int b0 = ch * per;; b0 += 32) {
-          const int b = b0 + lane;
-          int n = b < min((ch + 1) * per, p.B) ? tiles_of(p, b) : 0;
-          int sum = n;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(kFull, sum, o);
-            if (lane >= o) sum += up;
+    const bool ok = schedule_units<kTile>(
+        p, p.Hq, count, prefix, clc, bar_clc, bar_want, bar_ufull, bar_ufree, abort_flag, lane, asked, clc_n, [&](int slot, const SeqTile* s) {
+          VUnit w = {};
+          w.n_kv = -1;
+          if (s) {
+            w.b = s->b;
+            w.h = s->h;
+            w.q_row = s->q0 + s->t * kTile;
+            w.rows = min(s->q1 - w.q_row, kTile);
+            w.k_row = s->k0;
+            w.len_k = s->k1 - s->k0;
+            w.lim0 = p.causal ? s->t * kTile + w.len_k - (s->q1 - s->q0) : w.len_k - 1;
+            // key tiles up to the last key that the tile's last row sees
+            const int max_key = p.causal ? min(w.lim0 + w.rows - 1, w.len_k - 1) : w.len_k - 1;
+            w.n_kv = max_key < 0 ? 0 : max_key / kTile + 1;
           }
-          const unsigned le = __ballot_sync(kFull, sum <= r);
-          if (le == kFull && b0 + 32 < (ch + 1) * per) {
-            r -= __shfl_sync(kFull, sum, 31);
-            continue;
-          }
-          const int at = min(__popc(le), 31);
-          nt = __shfl_sync(kFull, n, at);
-          r -= __shfl_sync(kFull, sum - n, at);
-          w.b = min(b0 + at, p.B - 1);
-          break;
-        }
-        const int q0 = offset_at(p.cu_q, w.b, p.Tq), q1 = offset_at(p.cu_q, w.b + 1, p.Tq);
-        const int k0 = offset_at(p.cu_k, w.b, p.Tk), k1 = offset_at(p.cu_k, w.b + 1, p.Tk);
-        const int t = max(nt - 1 - r, 0);  // longest rows first
-        w.q_row = q0 + t * kTile;
-        w.rows = min(q1 - w.q_row, kTile);
-        w.k_row = k0;
-        w.len_k = max(k1 - k0, 0);
-        const int shift = w.len_k - (q1 - q0);
-        w.lim0 = p.causal ? t * kTile + shift : w.len_k - 1;
-        // key tiles up to the last key that the tile's last row sees
-        const int max_key = p.causal ? min(w.lim0 + w.rows - 1, w.len_k - 1) : w.len_k - 1;
-        w.n_kv = max_key < 0 ? 0 : max_key / kTile + 1;
-        u = n_units;  // ask for the next one
-      }
-      if (!__all_sync(kFull, mbar_wait(bar_ufree + (k & 1), ((k >> 1) & 1) ^ 1, lim, abort_flag))) { ok = false; break; }
-      if (lane == 0) {
-        units[k & 1] = w;
-        mbar_arrive(bar_ufull + (k & 1));
-      }
-      __syncwarp();
-      if (last) break;
-    }
+          units[slot] = w;
+        });
     if (!ok && lane == 0) fail();
   } else if (warp == kProducer) {
     // ------------------------------------------------------------ producer
@@ -310,7 +206,10 @@ __global__ void __launch_bounds__(kVarThreads, 1)
         const VUnit w = units[k & 1];
         mbar_arrive(bar_ufree + (k & 1));
         if (w.n_kv < 0) break;
-        if (w.n_kv == 0) continue;
+        if (w.n_kv == 0) {
+          mbar_arrive(bar_want);
+          continue;
+        }
         const int g = w.h / p.group;
         // Q of the previous unit is read until its last QK completes
         if (nq > 0 && !mbar_wait(bar_qfree, (nq - 1) & 1, lim, abort_flag)) { ok = false; break; }
@@ -384,6 +283,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
           }
         }
         if (!ok) break;
+        mbar_arrive(bar_want);
         jt += w.n_kv;
         ++nq;
       }
@@ -486,21 +386,19 @@ __global__ void __launch_bounds__(kVarThreads, 1)
       if (n_kv == 0) continue;
       if (!wait_all(bar_q, nq & 1)) { ok = false; break; }
       const int end = len_k - (n_kv - 1) * kTile;  // rows of the last visited tile that are keys, if below 128
-      for (int j = 0; ok && j <= n_kv; ++j) {
-        if (j < n_kv) {
-          if (!issue_qk(jt + j)) { ok = false; break; }
-          if (j == n_kv - 1) {
-            if (elect_one()) tc_commit(bar_qfree);
-            __syncwarp();
-          }
-        }
-        if (j == 0) continue;
+      if (!issue_qk(jt)) { ok = false; break; }
+      for (int j = 1; j < n_kv; ++j) {
+        if (!issue_qk(jt + j)) { ok = false; break; }
         // PV_0 overwrites O: the softmax must have read the last unit's
         if (j == 1 && nq > 0 && !wait_all(bar_ofree, (nq - 1) & 1)) { ok = false; break; }
-        if (j == n_kv && end < kTile && !clear_tail(jt + j - 1, end)) { ok = false; break; }
         if (!issue_pv(jt + j - 1, j - 1)) { ok = false; break; }
       }
       if (!ok) break;
+      if (elect_one()) tc_commit(bar_qfree);  // (the last QK is done when this is)
+      __syncwarp();
+      if (n_kv == 1 && nq > 0 && !wait_all(bar_ofree, (nq - 1) & 1)) { ok = false; break; }
+      if (end < kTile && !clear_tail(jt + n_kv - 1, end)) { ok = false; break; }
+      if (!issue_pv(jt + n_kv - 1, n_kv - 1)) { ok = false; break; }
       if (elect_one()) tc_commit(bar_ofinal);
       __syncwarp();
       jt += n_kv;
@@ -609,20 +507,28 @@ __global__ void __launch_bounds__(kVarThreads, 1)
           const float nb = yref == -INFINITY ? 0.0f : -yref;
           uint32_t pk[32];
           float lp0 = 0.0f, lp1 = 0.0f;
+          // A quarter of the pairs runs on the FMA pipe, but not where keys are
+          // masked: the polynomial does not give 0 for them.
+          auto weights = [&](auto poly) {
 #pragma unroll
-          for (int cc = 0; cc < 64; cc += 2) {
-            float z0, z1, p0, p1;
-            ffma2(z0, z1, s[cc], s[cc + 1], c, nb);
-            if ((cc & 6) == 0 && !masked) {  // a quarter of the pairs on the FMA pipe
-              exp2_poly_x2<4>(p0, p1, z0, z1);
-            } else {  // (the polynomial does not give 0 for a masked key)
-              p0 = ex2_approx(z0);
-              p1 = ex2_approx(z1);
+            for (int cc = 0; cc < 64; cc += 2) {
+              float z0, z1, p0, p1;
+              ffma2(z0, z1, s[cc], s[cc + 1], c, nb);
+              if (poly.value && (cc & 6) == 0) {
+                exp2_poly_x2<kPolyDegree>(p0, p1, z0, z1);
+              } else {
+                p0 = ex2_approx(z0);
+                p1 = ex2_approx(z1);
+              }
+              lp0 += p0;
+              lp1 += p1;
+              pk[cc / 2] = pack_bf16x2(p0, p1);
             }
-            lp0 += p0;
-            lp1 += p1;
-            pk[cc / 2] = pack_bf16x2(p0, p1);
-          }
+          };
+          if (masked)
+            weights(std::false_type{});
+          else
+            weights(std::true_type{});
           l += lp0 + lp1;
           tmem_st16x2_32<64>(tP, pk);
         } else {

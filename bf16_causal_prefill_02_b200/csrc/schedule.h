@@ -115,18 +115,16 @@ inline int choose_head_group(int B, int Hq, int Hkv, int Sq, int Sk, int d_qk, i
   return bh;
 }
 
-// Packed prompts: heads whose units are interleaved.  All of them while the K
-// and V of all heads stay in L2 (the 96 MB of choose_head_group), else the
-// query heads of as few kv heads as make at least 4.
+// Packed prompts: heads whose units are interleaved.  All of them, which
+// balances best, while the K and V of all heads are below 256 MB; else the
+// query heads of as many kv heads as stay below.  (All heads against 4 at a
+// time: 32/8 heads, 4096 rows bf16 137 against 163 us, FP8 112 against 151;
+// MLA, 16 heads, 16384 rows and 168 MB of K and V 1418 against 1498 us.)
 inline int choose_varlen_head_group(int Hq, int Hkv, int64_t Tk, int d_qk, int d_v, int elem_bytes) {
-  if ((double)Hkv * Tk * (d_qk + d_v) * elem_bytes <= 96.0 * 1024 * 1024) return Hq;
-  const int group = Hq / Hkv;
-  int kv = 1;
-  while (kv * group < 4 && kv < Hkv) {
-    do ++kv;
-    while (Hkv % kv != 0);
-  }
-  return kv * group;
+  const double one = (double)Tk * (d_qk + d_v) * elem_bytes;
+  int kv = Hkv;
+  while (kv > 1 && (Hkv % kv != 0 || kv * one > 256.0 * 1024 * 1024)) --kv;
+  return Hq / Hkv * kv;
 }
 
 // Short sequences (at most 64 query tiles) run persistent: one CTA per SM,
