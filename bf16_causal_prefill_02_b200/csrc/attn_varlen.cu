@@ -690,6 +690,7 @@ cudaError_t launch_variant(const VarlenLaunch& a, cudaStream_t st) {
 
 cudaError_t launch_attention_varlen(const VarlenLaunch& a, cudaStream_t st) {
   if (a.p.max_tiles <= 0) return cudaSuccess;
+  if (a.pairs) return launch_attention_varlen_pp(a, st);
   if (a.dtype == 0) return a.dqk == 128 ? launch_variant<0, 128, 0, 0>(a, st) : launch_variant<0, 192, 0, 0>(a, st);
   const bool bs = a.block_scale != 0;
   if (a.dqk == 128) {

@@ -115,6 +115,22 @@ inline int choose_head_group(int B, int Hq, int Hkv, int Sq, int Sk, int d_qk, i
   return bh;
 }
 
+// Packed prompts: a bound on the query tiles of `rows` rows, which the host
+// knows without the offsets.
+inline int varlen_tiles(int64_t Tq, int64_t B, int rows) {
+  return Tq > 0 ? (int)((Tq + (rows - 1) * B) / rows) : 0;
+}
+
+// Packed prompts, BF16 at d = 128: two tiles per CTA (attn_varlen_pp.cu) where
+// there are enough units to keep the SMs even, and sequences long enough to
+// fill both tiles.  Measured against one tile per CTA (us, one / two):
+//   units of 256 rows  192: 33.0 / 34.1   376: 253 / 271   512: 239 / 243
+//   640: 202 / 199     752: 498 / 496     1024: 478 / 468  1952: 146 / 121
+//   41 sequences of 100 rows, 32 heads: 39 / 45.
+inline bool use_varlen_pairs(int64_t Tq, int64_t B, int Hq, int num_sms) {
+  return (int64_t)varlen_tiles(Tq, B, 2 * kTile) * Hq >= 4 * (int64_t)num_sms && Tq >= 2 * kTile * B;
+}
+
 // Packed prompts: heads whose units are interleaved.  All of them, which
 // balances best, while the K and V of all heads are below 256 MB; else the
 // query heads of as many kv heads as stay below.  (All heads against 4 at a

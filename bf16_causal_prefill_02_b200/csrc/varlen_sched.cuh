@@ -9,7 +9,7 @@
 // hardware for the next block (clusterlaunchcontrol.try_cancel) when the
 // producer has issued the current unit's last load: late enough that a CTA
 // with a long unit does not hold a second one that an idle CTA could run
-// (8192 rows, 4 heads: AFTER against 125 us when asked a whole unit ahead),
+// (8192 rows, 4 heads: 91 against 125 us when asked a whole unit ahead),
 // early enough for the answer to hide behind the stages still to be consumed.
 #pragma once
 #include <cstdint>

@@ -364,10 +364,11 @@ int zq_attn_varlen_fwd(const zq_varlen_args* a, void* stream) {
   int rc = validate_options(a);
   if (rc != ZQ_OK) return rc;
   // the grid (a bound on the query tiles, times Hq) stays in 31 bits
-  const int64_t max_tiles = a->total_q > 0 ? (a->total_q + 127 * (int64_t)a->B) / 128 : 0;
+  const int64_t max_tiles = zq::varlen_tiles(a->total_q, a->B, zq::kTile);
   if (max_tiles * a->Hq > 0x7FFF0000ll) return ZQ_ERR_SHAPE;
   if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->out) || !aligned16(a->lse)) return ZQ_ERR_ALIGN;
-  rc = check_device(nullptr);
+  int sms = 0;
+  rc = check_device(&sms);
   if (rc != ZQ_OK) return rc;
   zq::VarlenLaunch L;
   L.q = a->q;
@@ -378,6 +379,7 @@ int zq_attn_varlen_fwd(const zq_varlen_args* a, void* stream) {
   L.dtype = a->dtype;
   L.mode = a->softmax_mode;
   L.block_scale = a->block_scale;
+  L.pairs = a->dtype == ZQ_DTYPE_BF16 && a->d_qk == 128 && zq::use_varlen_pairs(a->total_q, a->B, a->Hq, sms);
   const bool fp8 = a->dtype == ZQ_DTYPE_FP8_E4M3;
   zq::VarlenParams& p = L.p;
   p.out = a->out;

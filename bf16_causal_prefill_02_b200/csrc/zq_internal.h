@@ -112,8 +112,10 @@ struct VarlenLaunch {
   const void* v;
   VarlenParams p;
   int dqk, dtype, mode, block_scale;
+  bool pairs;  // two query tiles per CTA (BF16, d = 128)
 };
 cudaError_t launch_attention_varlen(const VarlenLaunch& a, cudaStream_t st);
+cudaError_t launch_attention_varlen_pp(const VarlenLaunch& a, cudaStream_t st);
 
 // A paged cache as the kernels address it: key c of sequence b is row
 // c & (page_size - 1) of page block_table[b * table_stride + (c >> page_shift)].

@@ -78,7 +78,7 @@ class Pack:
             if c is None:
                 assert (o == 0).all() and torch.isneginf(l).all()
                 continue
-            r = np.arange(self.hq * c.Sq) if rows is None or c.Sq <= 1024 else workloads.sample_rows(1, self.hq, c.Sq, every=rows).numpy()
+            r = np.arange(self.hq * c.Sq) if rows is None or c.Sq <= 256 else workloads.sample_rows(1, self.hq, c.Sq, every=rows).numpy()
             got.append(c.gather(o[None], l[None], r))
             want1.append(c.r1(r))
             want2.append(c.r2(r) if c.fp8 else want1[-1])
@@ -187,6 +187,36 @@ def test_fp8_equals_the_fixed_batch_kernel_bit_for_bit(dtype, dqk):
     ov, lv = zq.attn_varlen(q, k, v, cu, cu, softmax_mode=mode, **ds)
     assert torch.equal(ov.view(2, 700, 4, 128), o)
     assert torch.equal(lv.view(4, 2, 700).transpose(0, 1), l)
+
+
+# At least 4 x 148 units of 256 rows and 256 rows a sequence: two query tiles
+# per CTA (BF16, d = 128), here with both tiles, one, and none of a pair in use.
+MANY = [(1, 1), (700, 700), (0, 5), (257, 257), (256, 256), (128, 128), (900, 1400), (385, 60), (3, 0), (1500, 1501), (641, 641)]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hkv", [(48, 6), (32, 32), (40, 8)])
+def test_two_tiles_per_cta(hq, hkv, causal):
+    p = Pack(MANY, hq, hkv, 128, "bf16", causal, seed=200, front=3, back=130)
+    a = p.args()
+    assert a["q"].shape[0] >= 256 * len(MANY) and (a["q"].shape[0] + 255 * len(MANY)) // 256 * hq >= 4 * 148
+    out = torch.full((a["q"].shape[0], hq, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    _, lse = _zq().attn_varlen(out=out, **a)
+    p.check(out, lse, rows=61 if causal else 131)
+    last = int(p.cu(0)[-1])
+    assert (out[:3] == 3).all() and (out[last:] == 3).all()
+    again, lse2 = _zq().attn_varlen(**a)
+    assert torch.equal(again[3:last], out[3:last]) and torch.equal(lse2[:, 3:last], lse[:, 3:last])
+
+
+def test_two_tiles_per_cta_beside_a_sequence_of_nan():
+    p = Pack([(300, 300), (333, 333), (800, 800), (700, 700)], 64, 8, 128, "bf16", seed=220)
+    a = p.args()
+    assert (a["q"].shape[0] + 255 * 4) // 256 * 64 >= 4 * 148
+    for x in "qkv":
+        a[x][300:633] = float("nan")
+    out, lse = _zq().attn_varlen(**a)
+    p.check(out, lse, rows=61, only=(0, 2, 3))
 
 
 def test_no_keys_and_no_queries():
