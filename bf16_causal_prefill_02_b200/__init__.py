@@ -147,6 +147,7 @@ def _load():
 
 
 _lib = _load()
+_DECODE_WORKSPACE = int(_lib.zq_decode_workspace_bytes())  # a constant of the library
 
 
 def header_functions() -> list[str]:
@@ -571,10 +572,11 @@ def _on(device, stream, call):
         return call(stream.cuda_stream)
 
 
-def _check_on(device, *named):
-    """Every given (name, tensor) lives on CUDA device `device` (an index; -1: the host, which is refused)."""
-    for name, t in named:
-        if t is not None and (device < 0 or t.get_device() != device):
+def _check_on(device, names, *tensors):
+    """Every given tensor lives on CUDA device `device` (an index; -1: the host, which is refused)."""
+    for t in tensors:
+        if t is not None and (t.get_device() != device or device < 0):
+            name = [n for n, x in zip(names.split(), tensors) if x is t][0]
             if not t.is_cuda:
                 raise ValueError("%s must be a CUDA tensor" % name)
             raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, device))
@@ -603,54 +605,53 @@ def attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, out=None, lse=None, softmax
     Returns (out bf16 (total_q,Hq,d_v), lse fp32 (Hq,total_q) or None); rows
     of no sequence are not written."""
     torch = _torch()
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dim() != 3:
-            raise ValueError("%s must be 3-D (rows, heads, dim), got %d-D" % (name, t.dim()))
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
+    qs, ks, vs = q.shape, k.shape, v.shape
+    if len(qs) != 3 or len(ks) != 3 or len(vs) != 3:
+        raise ValueError("q, k and v must be 3-D (rows, heads, dim), got %d-D, %d-D, %d-D" % (len(qs), len(ks), len(vs)))
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("q, k and v must be contiguous")
     if q.dtype == k.dtype == v.dtype == torch.bfloat16:
         dtype = ZQ_DTYPE_BF16
     elif _is_fp8(q) and _is_fp8(k) and _is_fp8(v):
         dtype = ZQ_DTYPE_FP8_E4M3
     else:
         raise TypeError("q, k, v must all be bfloat16 or all FP8 e4m3")
-    Tq, Hq, dqk = q.shape
-    Tk, Hkv, _ = k.shape
-    dv = v.shape[2]
-    if k.shape[2] != dqk:
-        raise ValueError("k must have q's head dim %d, got %d" % (dqk, k.shape[2]))
-    if v.shape[0] != Tk or v.shape[1] != Hkv:
-        raise ValueError("v must have k's rows and head count (%d, %d), got (%d, %d)" % (Tk, Hkv, v.shape[0], v.shape[1]))
+    Tq, Hq, dqk = qs
+    Tk, Hkv, kd = ks
+    vr, vh, dv = vs
+    if kd != dqk:
+        raise ValueError("k must have q's head dim %d, got %d" % (dqk, kd))
+    if vr != Tk or vh != Hkv:
+        raise ValueError("v must have k's rows and head count (%d, %d), got (%d, %d)" % (Tk, Hkv, vr, vh))
     n = cu_seqlens_q.numel()
-    for name, t in (("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_k", cu_seqlens_k)):
-        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or n < 2 or t.numel() != n:
-            raise ValueError("%s must be a contiguous 1-D int32 tensor of B + 1 offsets, as long as the other" % name)
+    if (n < 2 or cu_seqlens_q.shape != (n,) or cu_seqlens_k.shape != (n,) or not cu_seqlens_q.dtype == cu_seqlens_k.dtype == torch.int32
+            or not (cu_seqlens_q.is_contiguous() and cu_seqlens_k.is_contiguous())):
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must be contiguous 1-D int32 tensors of B + 1 offsets each")
     B = n - 1
     if out is not None:
         _check_buffer("out", out, (Tq, Hq, dv), torch.bfloat16)
     if lse is not None:
         _check_buffer("lse", lse, (Hq, Tq), torch.float32)
-    layout = ZQ_DESCALE_PER_TENSOR
+    device = q.get_device()
+    layout, qd, kd, vd = ZQ_DESCALE_PER_TENSOR, None, None, None
     if dtype == ZQ_DTYPE_FP8_E4M3:
         for name, t in (("q_descale", q_descale), ("k_descale", k_descale), ("v_descale", v_descale)):
             if t is not None and (t.dtype != torch.float32 or not t.is_contiguous()):
                 raise ValueError("%s must be a contiguous float32 tensor" % name)
         layout = _descale_layout(B, Hkv, q_descale, k_descale, v_descale)
-    else:
-        q_descale = k_descale = v_descale = None
+        _check_on(device, "q_descale k_descale v_descale", q_descale, k_descale, v_descale)
+        qd, kd, vd = _ptr(q_descale), _ptr(k_descale), _ptr(v_descale)
     if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
         raise ValueError("status must be an int32 tensor with at least one element")
-    device = q.get_device()
-    _check_on(device, ("q", q), ("k", k), ("v", v), ("cu_seqlens_q", cu_seqlens_q), ("cu_seqlens_k", cu_seqlens_k), ("out", out),
-              ("lse", lse), ("q_descale", q_descale), ("k_descale", k_descale), ("v_descale", v_descale), ("status", status))
+    _check_on(device, "q k v cu_seqlens_q cu_seqlens_k out lse status", q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, status)
+    scale = float(softmax_scale) if softmax_scale else 0.0
 
     def call(s):
         o = q.new_empty((Tq, Hq, dv), dtype=torch.bfloat16) if out is None else out
         e = q.new_empty((Hq, Tq), dtype=torch.float32) if lse is None and return_lse else lse
         a = zq_varlen_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(e), cu_seqlens_q.data_ptr(),
-                           cu_seqlens_k.data_ptr(), B, Tq, Tk, Hq, Hkv, dqk, dv, float(softmax_scale) if softmax_scale else 0.0,
-                           int(bool(causal)), dtype, _ptr(q_descale), _ptr(k_descale), _ptr(v_descale), int(softmax_mode),
-                           int(bool(block_scale)), int(headroom_T), _ptr(status), layout)
+                           cu_seqlens_k.data_ptr(), B, Tq, Tk, Hq, Hkv, dqk, dv, scale, 1 if causal else 0, dtype, qd, kd, vd,
+                           int(softmax_mode), 1 if block_scale else 0, int(headroom_T), _ptr(status), layout)
         _check(zq_attn_varlen_fwd(a, s), "zq_attn_varlen_fwd")
         return o, e
 
@@ -670,7 +671,8 @@ def flash_attn_varlen_func(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q=Non
 def _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale):
     """The zq_paged_kv of these tensors."""
     torch = _torch()
-    if k_cache.dim() != 4 or v_cache.dim() != 4:
+    kshape, vshape = k_cache.shape, v_cache.shape
+    if len(kshape) != 4 or len(vshape) != 4:
         raise ValueError("k_cache and v_cache must be 4-D (pages, page size, kv heads, dim)")
     if k_cache.dtype == v_cache.dtype == torch.bfloat16:
         dtype = ZQ_DTYPE_BF16
@@ -678,9 +680,9 @@ def _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale
         dtype = ZQ_DTYPE_FP8_E4M3
     else:
         raise TypeError("k_cache and v_cache must both be bfloat16 or both FP8 e4m3")
-    pages, page_size, Hkv, dqk = k_cache.shape
-    vpages, vpage_size, vHkv, dv = v_cache.shape
-    if vpages != pages or vpage_size != page_size or vHkv != Hkv:
+    pages, page_size, Hkv, dqk = kshape
+    dv = vshape[3]
+    if vshape[:3] != kshape[:3]:
         raise ValueError("v_cache must have k_cache's pages, page size and heads %s, got %s"
                          % (tuple(k_cache.shape[:3]), tuple(v_cache.shape[:3])))
     if block_table.dim() != 2 or block_table.dtype != torch.int32:
@@ -696,9 +698,9 @@ def _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale
             if t is not None and (t.dtype != torch.float32 or not t.is_contiguous()):
                 raise ValueError("%s must be a contiguous float32 tensor" % name)
         per_head = _descale_layout(1, Hkv, k_descale, v_descale)
-        _check_on(device, ("k_descale", k_descale), ("v_descale", v_descale))
+        _check_on(device, "k_descale v_descale", k_descale, v_descale)
         kd, vd = _ptr(k_descale), _ptr(v_descale)
-    _check_on(device, ("k_cache", k_cache), ("v_cache", v_cache), ("block_table", block_table), ("cache_seqlens", cache_seqlens))
+    _check_on(device, "k_cache v_cache block_table cache_seqlens", k_cache, v_cache, block_table, cache_seqlens)
     return zq_paged_kv(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, block_table.data_ptr(), cache_seqlens.data_ptr(),
                        kd, vd, ts, width, pages, page_size, B, Hkv, dqk, dv, dtype, per_head), device, B, Hkv, dqk, dv
 
@@ -729,7 +731,7 @@ def kv_append(k, v, k_cache, v_cache, block_table, cache_seqlens, cu_seqlens=Non
     elif cu_seqlens.dtype != torch.int32 or cu_seqlens.shape != (B + 1,) or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must be a contiguous int32 tensor of %d offsets" % (B + 1))
     ks, vs = _row_stride("k", k), _row_stride("v", v)
-    _check_on(device, ("k", k), ("v", v), ("cu_seqlens", cu_seqlens))
+    _check_on(device, "k v cu_seqlens", k, v, cu_seqlens)
     kp, vp, cp = k.data_ptr(), v.data_ptr(), _ptr(cu_seqlens)
     _on(device, stream, lambda s: _check(zq_kv_append(c, kp, vp, ks, vs, cp, T, s), "zq_kv_append"))
     return k_cache, v_cache
@@ -746,18 +748,19 @@ def attn_decode(q, k_cache, v_cache, block_table, cache_seqlens, out=None, lse=N
     c, device, B, Hkv, dqk, dv = _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale)
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be bfloat16")
-    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != dqk:
-        raise ValueError("q must have shape (%d, heads, %d), got %s" % (B, dqk, tuple(q.shape)))
-    Hq = q.shape[1]
+    qshape = q.shape
+    if len(qshape) != 3 or qshape[0] != B or qshape[2] != dqk:
+        raise ValueError("q must have shape (%d, heads, %d), got %s" % (B, dqk, tuple(qshape)))
+    Hq = qshape[1]
     if out is not None:
         _check_buffer("out", out, (B, Hq, dv), torch.bfloat16)
     if lse is not None:
         _check_buffer("lse", lse, (B, Hq), torch.float32)
-    nbytes = zq_decode_workspace_bytes()
+    nbytes = _DECODE_WORKSPACE
     if workspace is not None and (workspace.numel() * workspace.element_size() < nbytes or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous and hold zq_decode_workspace_bytes() bytes")
     qs = _row_stride("q", q)
-    _check_on(device, ("q", q), ("out", out), ("lse", lse), ("workspace", workspace))
+    _check_on(device, "q out lse workspace", q, out, lse, workspace)
     scale = float(softmax_scale) if softmax_scale else 0.0
 
     def call(s):

@@ -140,6 +140,7 @@ struct AppendLaunch {
   int64_t k_stride, v_stride;  // bytes between tokens
   const int32_t* cu;           // B + 1 token offsets, or nullptr (token t is sequence t's)
   int64_t T;
+  int shares;  // warps per token (set by the launcher)
 };
 cudaError_t launch_kv_append(const AppendLaunch& a, cudaStream_t st);
 struct DecodeLaunch {
