@@ -144,6 +144,8 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     for (int i = threadIdx.x; i < G::ONES_BYTES / 4; i += kVarThreads) ones[i] = 0x38383838u;
     fence_proxy_async_smem();
   }
+  launch_dependents();
+  wait_previous_kernel();
   UnitCount count;  // (the scheduler's; beside the set-up of the others)
   if (warp == kScheduler) count = count_tiles<kTile>(p, prefix, lane);
   if (warp == kIssuer) {
@@ -682,8 +684,7 @@ cudaError_t launch_variant(const VarlenLaunch& a, cudaStream_t st) {
   auto kern = attn_varlen_kernel<DT, DQK, MODE, BS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)p.max_tiles * (unsigned)p.Hq, kVarThreads, G::SMEM, st>>>(mQ, mQ2, mK, mK2, mV, p);
-  return cudaGetLastError();
+  return launch_overlapped(kern, dim3((unsigned)p.max_tiles * (unsigned)p.Hq), dim3(kVarThreads), G::SMEM, st, mQ, mQ2, mK, mK2, mV, p);
 }
 
 }  // namespace

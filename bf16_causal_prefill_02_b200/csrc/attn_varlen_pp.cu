@@ -123,6 +123,8 @@ __global__ void __launch_bounds__(kVppThreads, 1)
     *abort_flag = 0;
     fence_barrier_init();
   }
+  launch_dependents();
+  wait_previous_kernel();
   UnitCount count;  // (the scheduler's; beside the set-up of the others)
   if (warp == kScheduler) count = count_tiles<2 * kTile>(p, reinterpret_cast<int*>(smem + G::OFF_PREFIX), lane);
   if (warp == kIssuer0) {
@@ -506,8 +508,7 @@ cudaError_t launch_attention_varlen_pp(const VarlenLaunch& a, cudaStream_t st) {
   auto kern = attn_varlen_pp_kernel;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)p.max_tiles * (unsigned)p.Hq, kVppThreads, G::SMEM, st>>>(mQ, mK, mV, p);
-  return cudaGetLastError();
+  return launch_overlapped(kern, dim3((unsigned)p.max_tiles * (unsigned)p.Hq), dim3(kVppThreads), G::SMEM, st, mQ, mK, mV, p);
 }
 
 }  // namespace zq

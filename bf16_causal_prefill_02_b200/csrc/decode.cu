@@ -49,7 +49,8 @@ constexpr int kMaxEntries = 1280;  // warps that the workspace has room for
 // a piece of many short segments gets fewer of them (64 sequences of 1 to 4096
 // keys, 32/8 heads bf16: 51 us with 1, 48 with 2, 44 with 4 and with 8).
 constexpr int kSegmentCost = 4;
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 4;
+constexpr int kJoinBatch = 8;  // parts' rows on their way at once
 constexpr int kJoinAlone = 24;  // parts that one warp joins by itself
 constexpr unsigned kJoinStep = 733;  // prime, and no divisor of a number of entries (at most 1280)
 
@@ -122,6 +123,7 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
   const int quad = lane >> 2, ql = lane & 3;
   const int heads = c.Hkv * p.head_tiles / p.team;  // teams of flat head tiles
   launch_dependents();
+  wait_previous_kernel();
 
   // ---- the line: b outermost, then the team's heads, then kSegmentCost
   // places without a tile and the key tiles
@@ -590,6 +592,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Deco
   auto entry = [&](int w) { return (int)(((blockIdx.x * kJoinWarps + w) * kJoinStep) % (gridDim.x * kJoinWarps)); };
   const int mine = entry(warp);
   const int stats = p.slot / (DV + 2) * DV;  // where a part's (m, l) begin
+  launch_dependents();
   wait_previous_kernel();
   // parts first, first + step, ...: 32 at a time, a lane each for (m, l), then
   // their O with weights that no longer depend on one another.  Slot 1 of the
@@ -597,8 +600,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Deco
   auto read = [&](Part& t, int at, int first, int step, int parts) {
     auto part = [&](int j) { return p.part + ((int64_t)(at + j * p.team) * 2 + (j == 0 ? 1 : 0)) * p.slot; };
     for (int j0 = first; j0 < parts; j0 += 32 * step) {
-      const int j = j0 + lane * step;
-      const float2 st = j < parts ? *reinterpret_cast<const float2*>(part(j) + stats + 2 * r) : make_float2(-INFINITY, 0.0f);
+      const int n = min((parts - j0 + step - 1) / step, 32);
+      auto o_of = [&](int i) { return reinterpret_cast<const float4*>(part(j0 + min(i, n - 1) * step) + r * DV)[lane]; };
+      const float2 st = lane < n ? *reinterpret_cast<const float2*>(part(j0 + lane * step) + stats + 2 * r) : make_float2(-INFINITY, 0.0f);
+      float4 v[kJoinBatch];
+#pragma unroll
+      for (int i = 0; i < kJoinBatch; ++i) v[i] = o_of(i);
       float m = st.x;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
@@ -607,18 +614,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Deco
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
       float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      const int n = min((parts - j0 + step - 1) / step, 32);
-      for (int i0 = 0; i0 < n; i0 += 8) {  // eight loads at once; the weights past the last are 0
-        float4 v[8];
+      for (int i0 = 0; i0 < n; i0 += kJoinBatch) {  // (the weights past the last part are 0)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = reinterpret_cast<const float4*>(part(j0 + min(i0 + i, n - 1) * step) + r * DV)[lane];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kJoinBatch; ++i) {
           const float fi = i0 + i < n ? __shfl_sync(kFull, f, i0 + i) : 0.0f;
           a.x += v[i].x * fi;
           a.y += v[i].y * fi;
           a.z += v[i].z * fi;
           a.w += v[i].w * fi;
+        }
+        if (i0 + kJoinBatch < n) {
+#pragma unroll
+          for (int i = 0; i < kJoinBatch; ++i) v[i] = o_of(i0 + kJoinBatch + i);
         }
       }
       t.add(make_float2(m, l), a);
@@ -671,20 +678,11 @@ cudaError_t launch_kernel(DecodeParams& p, cudaStream_t st, int num_sms) {
   auto kern = decode_kernel<DQK, FP8, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
   if (e != cudaSuccess) return e;
-  kern<<<grid, G::THREADS, G::SMEM, st>>>(p);
-  e = cudaGetLastError();
+  e = launch_overlapped(kern, dim3((unsigned)grid), dim3(G::THREADS), G::SMEM, st, p);
   if (e != cudaSuccess) return e;
   const int entries = grid * G::WARPS;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((entries + kJoinWarps - 1) / kJoinWarps), (unsigned)(p.group < kMaxHeads ? p.group : kMaxHeads));
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel, (const DecodeParams)p, entries);
+  const dim3 joins((unsigned)((entries + kJoinWarps - 1) / kJoinWarps), (unsigned)(p.group < kMaxHeads ? p.group : kMaxHeads));
+  return launch_overlapped(decode_join_kernel, joins, dim3(kJoinWarps * 32), 0, st, p, entries);
 }
 
 template <int DQK, int FP8>

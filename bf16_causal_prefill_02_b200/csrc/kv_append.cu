@@ -72,6 +72,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const Appe
   const int lane = threadIdx.x & 31;
   const int64_t share = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
   const int64_t t = share / a.shares;
+  launch_dependents();
+  wait_previous_kernel();
   if (t >= a.T) return;
   const PagedKV& c = a.c;
   const int nk = c.Hkv * (DQK / 8), nv = c.Hkv * (DV / 8);  // pieces of 8 elements
@@ -117,8 +119,7 @@ cudaError_t launch_kv_append(const AppendLaunch& a0, cudaStream_t st) {
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   auto kern = a.c.dtype == 1 ? (a.c.dqk == 128 ? kv_append_kernel<1, 128> : kv_append_kernel<1, 192>)
                              : (a.c.dqk == 128 ? kv_append_kernel<0, 128> : kv_append_kernel<0, 192>);
-  kern<<<(unsigned)blocks, kAppendWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(kern, dim3((unsigned)blocks), dim3(kAppendWarps * 32), 0, st, a);
 }
 
 }  // namespace zq

@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "attn_math.cuh"
+#include "sm100_ptx.cuh"
 #include "zq_internal.h"
 
 namespace zq {
@@ -58,9 +59,5 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Programmatic dependent launch: let the next kernel of the stream start its
-// blocks / wait until the previous kernel's writes are visible.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 }  // namespace zq

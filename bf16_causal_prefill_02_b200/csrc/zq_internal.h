@@ -87,6 +87,25 @@ struct QuantItems {
 cudaError_t launch_quantize_multi(QuantItems Q, int count, void* workspace, cudaStream_t st, int num_sms);
 void* noalloc_scratch_for_device(int dev);
 
+// A launch whose blocks may become resident while the stream's previous kernel
+// still runs.  The kernel calls griddepcontrol.wait before it touches memory,
+// which returns once that kernel's writes are visible; nothing else changes in
+// the stream's order.
+template <class... P, class... A>
+inline cudaError_t launch_overlapped(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
 // Attention over packed prompts.
 struct VarlenParams {
   void* out;   // (Tq, Hq, d_v) bfloat16
