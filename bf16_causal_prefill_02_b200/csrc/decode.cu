@@ -50,6 +50,7 @@ constexpr int kMaxEntries = 1280;  // warps that the workspace has room for
 // keys, 32/8 heads bf16: 51 us with 1, 48 with 2, 44 with 4 and with 8).
 constexpr int kSegmentCost = 4;
 constexpr int kJoinWarps = 4;
+constexpr int kItemWarps = 8;
 constexpr int kJoinBatch = 8;  // parts' rows on their way at once
 constexpr int kJoinAlone = 24;  // parts that one warp joins by itself
 constexpr unsigned kJoinStep = 733;  // prime, and no divisor of a number of entries (at most 1280)
@@ -65,7 +66,11 @@ struct DecodeParams {
   int team;      // warps that walk the same keys of adjacent heads: 1, 2 or 4, dividing the flat head tiles
   int slot;      // floats of a part: O of 8 or 16 heads, then their (m, l)
   // workspace: who cuts what, then the parts
-  int4* cut;     // [piece][team] {sequence, flat head tile, parts, 0} of the segment that this piece begins and does not finish
+  // {sequence, flat head tile, parts, first part's entry} of a (sequence, head
+  // tile) that is cut, parts = 0 where it is not: one per (sequence, head tile)
+  // where by_item, else one per entry [piece][team], of the one it begins
+  int4* cut;
+  int by_item;
   float* part;   // [piece][team][2][slot]: slot 0 a segment begun by an earlier piece, slot 1 one left to later pieces
 };
 
@@ -155,8 +160,12 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
       if (w < warp) before += scan[w];
       line += scan[w];
     }
-    // no more pieces than places, so that none is empty
-    pieces = (int)min((int64_t)gridDim.x * per_cta, line);
+    // No more pieces than places, so that none is empty, nor so many of one
+    // (sequence, head) that joining them costs more than a longer piece: about
+    // 0.5 us a tile against 0.02 us a part (8/2 heads bf16, 2 x 11382 keys:
+    // 17.8 us with the 296 parts that the warps allow, 13.1 with 143).
+    const int least = max((int)sqrtf((float)(line / ((int64_t)c.B * heads)) * (1.0f / 22.0f)), 1);
+    pieces = (int)min((int64_t)gridDim.x * per_cta, max(line / least, (int64_t)1));
     const int64_t at0 = before + sum - mine;  // place of this thread's first sequence
     for (int w = 0; w < per_cta; ++w) {
       const int pw = w * gridDim.x + blockIdx.x;
@@ -182,6 +191,8 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
   // sequences without keys: 0 and -inf
   for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
     if (keys_of(c, b) > 0) continue;
+    if (p.by_item)
+      for (int i = threadIdx.x; i < c.Hkv * p.head_tiles; i += THREADS) p.cut[b * c.Hkv * p.head_tiles + i] = make_int4(0, 0, 0, 0);
     for (int i = threadIdx.x; i < p.Hq * DV / 2; i += THREADS)
       reinterpret_cast<uint32_t*>(p.out + (int64_t)b * p.Hq * DV)[i] = 0u;
     if (p.lse)
@@ -220,7 +231,7 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
     const char* kbase = c.k + (int64_t)g * (DQK * G::ES);
     const char* vbase = c.v + (int64_t)g * (DV * G::ES);
     const int page_mask = (1 << c.page_shift) - 1;
-    const bool whole = G::KEYS <= page_mask + 1;  // a tile lies in one page
+    const bool whole = page_mask >= 15;  // each 16-key block of a tile lies in one page
     // the page of key (step, lane % KEYS), or -1: not there
     auto page_at = [&](int step) -> int {
       const int key = key0 + step * G::KEYS + (lane & (G::KEYS - 1));
@@ -228,21 +239,14 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
       if (step < steps && key < len) pg = table[key >> c.page_shift];
       return (unsigned)pg < (unsigned)c.num_pages ? pg : -1;
     };
-    unsigned have[NS];  // which keys of each stage are there
-    auto load = [&](int step, int s, int pg) {
+    // starts the loads of a tile into the stage at sk; returns which of its keys are there
+    auto load = [&](int step, uint32_t sk, int pg) -> unsigned {
       const unsigned vm = __ballot_sync(kFull, pg >= 0) & G::ALL;
-#pragma unroll
-      for (int i = 0; i < NS; ++i)
-        if (i == s) have[i] = vm;
-      const uint32_t sk = ring_u + s * G::STAGE, sv = sk + G::KBYTES;
+      const uint32_t sv = sk + G::KBYTES;
       const int kb = key0 + step * G::KEYS;
       if (whole) {
-        // the tile lies in one page: rows at fixed distances.  Where a row is
-        // 8, 16 or 32 pieces, the lane's piece is the same in all of them.
-        const int64_t page = max(__shfl_sync(kFull, pg, 0), 0);  // (a tile's first key is there if any is)
-        const int64_t row = kb & page_mask;
-        const char* ks = kbase + page * c.k_page + row * krow;
-        const char* vs = vbase + page * c.v_page + row * vrow;
+        // rows of a block at fixed distances.  Where a row is 8, 16 or 32
+        // pieces, the lane's piece is the same in all of them.
         auto rows_of = [&](auto all) {
           auto copy = [&](uint32_t dst, const char* src, int r) {
             if constexpr (all.value)
@@ -250,24 +254,31 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
             else
               cp_async16(dst, src, (vm >> r) & 1u ? 16 : 0);
           };
-          if constexpr (32 % G::KCH == 0) {
-            constexpr int R = 32 / G::KCH;
-            const int r0 = lane / G::KCH, ch = lane % G::KCH;
-            const char* src = ks + r0 * krow + ch * 16;
 #pragma unroll
-            for (int i = 0; i < G::KEYS / R; ++i, src += R * krow) copy(sk + G::at_k(r0 + R * i, ch), src, r0 + R * i);
-          } else {
+          for (int blk = 0; blk < G::KB; ++blk) {
+            const int64_t page = max(__shfl_sync(kFull, pg, blk * 16), 0);  // (a block's first key is there if any is)
+            const int64_t row = (kb + blk * 16) & page_mask;
+            const char* ks = kbase + page * c.k_page + row * krow;
+            const char* vs = vbase + page * c.v_page + row * vrow;
+            if constexpr (32 % G::KCH == 0) {
+              constexpr int R = 32 / G::KCH;
+              const int r0 = lane / G::KCH, ch = lane % G::KCH;
+              const char* src = ks + r0 * krow + ch * 16;
 #pragma unroll
-            for (int i = 0; i < G::KEYS * G::KCH / 32; ++i) {
-              const int idx = i * 32 + lane, r = idx / G::KCH, ch = idx % G::KCH;
-              copy(sk + G::at_k(r, ch), ks + r * krow + ch * 16, r);
+              for (int i = 0; i < 16; i += R, src += R * krow) copy(sk + G::at_k(blk * 16 + i + r0, ch), src, blk * 16 + i + r0);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16 * G::KCH / 32; ++i) {
+                const int idx = i * 32 + lane, r = idx / G::KCH, ch = idx % G::KCH;
+                copy(sk + G::at_k(blk * 16 + r, ch), ks + r * krow + ch * 16, blk * 16 + r);
+              }
             }
-          }
-          constexpr int R = 32 / G::VCH;
-          const int r0 = lane / G::VCH, ch = lane % G::VCH;
-          const char* src = vs + r0 * vrow + ch * 16;
+            constexpr int R = 32 / G::VCH;
+            const int r0 = lane / G::VCH, ch = lane % G::VCH;
+            const char* src = vs + r0 * vrow + ch * 16;
 #pragma unroll
-          for (int i = 0; i < G::KEYS / R; ++i, src += R * vrow) copy(sv + G::at_v(r0 + R * i, ch), src, r0 + R * i);
+            for (int i = 0; i < 16; i += R, src += R * vrow) copy(sv + G::at_v(blk * 16 + i + r0, ch), src, blk * 16 + i + r0);
+          }
         };
         if (vm == G::ALL)
           rows_of(std::true_type{});
@@ -285,15 +296,8 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
           cp_async16(sv + G::at_v(r, ch), vbase + max(rp, 0) * c.v_page + ((kb + r) & page_mask) * vrow + ch * 16, rp >= 0 ? 16 : 0);
         }
       }
+      return vm;
     };
-    int pg = page_at(0);
-#pragma unroll
-    for (int s = 0; s < NS - 1; ++s) {
-      if (s < steps) load(s, s, pg);
-      cp_async_commit();
-      pg = page_at(s + 1);
-    }
-
     // ---- queries as B fragments: column (head) quad of each product, and the
     // score scale of the columns 2 ql, 2 ql + 1 that this lane holds of S^T
     uint32_t qb[NT][G::QK_STEPS][2];
@@ -357,19 +361,31 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
       l[nt][0] = l[nt][1] = 0.0f;
     }
 
-    for (int st0 = 0; st0 < steps; st0 += NS) {
+    // One body for the filling, the steady state and the draining of the ring:
+    // it loads tile `it` and works on tile it - (NS - 1).  (Unrolled over the
+    // stages the code outgrew the instruction cache: 16/1 heads e4m3, 30 x
+    // 13000 keys, 43.0 against 39.8 us.)
+    unsigned have[NS];  // keys that are there, of tiles it - (NS - 1) .. it
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const int st = st0 + s;
-        if (st >= steps) break;
-        // the stage of step st - 1 is free: refill it, then wait for this one
+    for (int i = 0; i < NS; ++i) have[i] = 0u;
+    uint32_t s_load = 0, s_work = 0;  // stages, as byte offsets
+    int pg = page_at(0);
+#pragma unroll 1
+    for (int it = 0; it < steps + NS - 1; ++it) {
+      {
+        // (the stage to be filled is that of the tile worked on last)
         __syncwarp();
-        if (st + NS - 1 < steps) load(st + NS - 1, (s + NS - 1) % NS, pg);
+#pragma unroll
+        for (int i = 0; i + 1 < NS; ++i) have[i] = have[i + 1];
+        have[NS - 1] = it < steps ? load(it, ring_u + s_load, pg) : 0u;
         cp_async_commit();
-        pg = page_at(st + NS);
+        pg = page_at(it + 1);
+        s_load = s_load + G::STAGE == G::RING ? 0 : s_load + G::STAGE;
+        if (it < NS - 1) continue;
         cp_async_wait<NS - 1>();
         __syncwarp();
-        const uint32_t sk = ring_u + s * G::STAGE, sv = sk + G::KBYTES;
+        const uint32_t sk = ring_u + s_work, sv = sk + G::KBYTES;
+        s_work = s_work + G::STAGE == G::RING ? 0 : s_work + G::STAGE;
 
         // S^T = K Q^T: of each 16 keys the lane holds quad (i < 2) and quad + 8 of heads 2 ql + (i & 1)
         float sc[NT][G::KB][4];
@@ -401,7 +417,7 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
           }
         }
         // log2 domain, mask
-        const unsigned vm = have[s];
+        const unsigned vm = have[0];
         float mx[NT][2];
         bool move = false;
 #pragma unroll
@@ -550,14 +566,18 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
       }
       __syncwarp();
     }
-    if (begins && !ends) {
+    if (begins) {
       // its parts: this piece's and those up to the one of its last place.
       // The piece of place y is the largest j with floor(line * j / pieces) <= y.
       const int64_t j = ((start + span) * pieces - 1) / line;
-      cut = make_int4(b, fh, (int)(j - piece) + 1, 0);
+      const int4 mine = make_int4(b, fh, ends ? 0 : (int)(j - piece) + 1, mine_at);
+      if (!p.by_item)
+        cut = ends ? cut : mine;
+      else if (lane == 0)
+        p.cut[b * c.Hkv * p.head_tiles + fh] = mine;
     }
   }
-  if (lane == 0) p.cut[mine_at] = cut;
+  if (!p.by_item && lane == 0) p.cut[mine_at] = cut;
 }
 
 // Running (m, l, O) of a row, a lane's four channels of O.
@@ -576,21 +596,21 @@ struct Part {
   }
 };
 
-// Joins the parts of the segments that were cut; blockIdx.y is the query head
-// in the head tile.  A warp joins the few parts of its own entry's segment
-// alone; the parts of a segment with many are shared by the block's warps.
-// Entries are dealt to the blocks in an order that is not theirs (a multiple
-// modulo their number), because those of a team, or of equally long sequences,
-// are cut at regular distances.
-__global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const DecodeParams p, int entries) {
-  constexpr int DV = 128;
+// Joins the parts of what was cut; blockIdx.y is the query head in the head
+// tile.  BY_ITEM: a block for each (sequence, head tile), its warps share the
+// parts.  Else a warp for each entry, which joins
+// a few parts alone; the parts of one with many are shared by the block's
+// warps.  Entries are dealt to the blocks in an order that is not theirs (a
+// multiple modulo their number), because those of a team, or of equally long
+// sequences, are cut at regular distances.
+template <int BY_ITEM>
+__global__ void __launch_bounds__((BY_ITEM ? kItemWarps : kJoinWarps) * 32) decode_join_kernel(const DecodeParams p, int entries) {
+  constexpr int DV = 128, WARPS = BY_ITEM ? kItemWarps : kJoinWarps;
   constexpr unsigned kFull = 0xffffffffu;
-  __shared__ float4 acc_s[kJoinWarps][32];
-  __shared__ float2 stat_s[kJoinWarps];
-  __shared__ int4 cut_s[kJoinWarps];
+  __shared__ float4 acc_s[WARPS][32];
+  __shared__ float2 stat_s[WARPS];
+  __shared__ int4 cut_s[WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y;
-  auto entry = [&](int w) { return (int)(((blockIdx.x * kJoinWarps + w) * kJoinStep) % (gridDim.x * kJoinWarps)); };
-  const int mine = entry(warp);
   const int stats = p.slot / (DV + 2) * DV;  // where a part's (m, l) begin
   launch_dependents();
   wait_previous_kernel();
@@ -641,30 +661,40 @@ __global__ void __launch_bounds__(kJoinWarps * 32) decode_join_kernel(const Deco
         empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(t.a.x * inv, t.a.y * inv), pack_bf16x2(t.a.z * inv, t.a.w * inv));
     if (p.lse && lane == 0) p.lse[row] = empty ? -INFINITY : (t.m + log2f(t.l)) * 0.6931471805599453f;
   };
-  int4 d = mine < entries ? p.cut[mine] : make_int4(0, 0, 0, 0);
-  if (r >= min(kMaxHeads, p.group - (d.y % p.head_tiles) * kMaxHeads)) d.z = 0;
-  if (d.z > 0 && d.z <= kJoinAlone) {
+  auto share = [&](int4 e) {
     Part t;
-    read(t, mine, 0, 1, d.z);
-    write(t, d);
-  }
-  if (lane == 0) cut_s[warp] = d;
-  __syncthreads();
-  for (int w = 0; w < kJoinWarps; ++w) {
-    const int4 e = cut_s[w];
-    if (e.z <= kJoinAlone) continue;
-    Part t;
-    read(t, entry(w), warp, kJoinWarps, e.z);
+    read(t, e.w, warp, WARPS, e.z);
     acc_s[warp][lane] = t.a;
     if (lane == 0) stat_s[warp] = make_float2(t.m, t.l);
     __syncthreads();
     if (warp == 0) {
       Part all;
 #pragma unroll
-      for (int v = 0; v < kJoinWarps; ++v) all.add(stat_s[v], acc_s[v][lane]);
+      for (int v = 0; v < WARPS; ++v) all.add(stat_s[v], acc_s[v][lane]);
       write(all, e);
     }
+  };
+  auto rows_of = [&](int4 e) { return min(kMaxHeads, p.group - (e.y % p.head_tiles) * kMaxHeads); };
+  if constexpr (BY_ITEM) {
+    const int4 d = p.cut[blockIdx.x];
+    if (d.z > 0 && r < rows_of(d)) share(d);
+  } else {
+    const int mine = (int)(((blockIdx.x * WARPS + warp) * kJoinStep) % (gridDim.x * WARPS));
+    int4 d = mine < entries ? p.cut[mine] : make_int4(0, 0, 0, 0);
+    if (r >= rows_of(d)) d.z = 0;
+    if (d.z > 0 && d.z <= kJoinAlone) {
+      Part t;
+      read(t, d.w, 0, 1, d.z);
+      write(t, d);
+    }
+    if (lane == 0) cut_s[warp] = d;
     __syncthreads();
+    for (int w = 0; w < WARPS; ++w) {
+      const int4 e = cut_s[w];
+      if (e.z <= kJoinAlone) continue;
+      share(e);
+      __syncthreads();
+    }
   }
 }
 
@@ -675,14 +705,23 @@ cudaError_t launch_kernel(DecodeParams& p, cudaStream_t st, int num_sms) {
   // one piece per warp of the CTAs that are resident at once
   constexpr int most = kMaxEntries / G::WARPS;
   const int grid = num_sms * kCtasPerSm < most ? num_sms * kCtasPerSm : most;
+  const int entries = grid * G::WARPS;
+  const int64_t items = (int64_t)p.c.B * p.c.Hkv * p.head_tiles;
+  // Blocks of a (sequence, head tile) each where there are few, which then have
+  // many parts (us, by item / by entry: 2 x 11382 keys 8/2 heads 13.1 / 17.8,
+  // 11 x 244 keys 16/1 heads 10.2 / 14.5; but 19 x 70 keys 32/8 heads, 608
+  // blocks, 11.4 / 9.9 and 86 x 1000 keys, 2752 blocks, 70 / 61).
+  const int rows = p.group < kMaxHeads ? p.group : kMaxHeads;
+  p.by_item = items * rows <= 4 * num_sms && items <= entries ? 1 : 0;
   auto kern = decode_kernel<DQK, FP8, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
   if (e != cudaSuccess) return e;
   e = launch_overlapped(kern, dim3((unsigned)grid), dim3(G::THREADS), G::SMEM, st, p);
   if (e != cudaSuccess) return e;
-  const int entries = grid * G::WARPS;
-  const dim3 joins((unsigned)((entries + kJoinWarps - 1) / kJoinWarps), (unsigned)(p.group < kMaxHeads ? p.group : kMaxHeads));
-  return launch_overlapped(decode_join_kernel, joins, dim3(kJoinWarps * 32), 0, st, p, entries);
+  if (p.by_item)
+    return launch_overlapped(decode_join_kernel<1>, dim3((unsigned)items, (unsigned)rows), dim3(kItemWarps * 32), 0, st, p, entries);
+  const unsigned blocks = (unsigned)((entries + kJoinWarps - 1) / kJoinWarps);
+  return launch_overlapped(decode_join_kernel<0>, dim3(blocks, (unsigned)rows), dim3(kJoinWarps * 32), 0, st, p, entries);
 }
 
 template <int DQK, int FP8>
