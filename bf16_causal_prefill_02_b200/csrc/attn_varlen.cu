@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
   uint64_t* bar_clc = bar_ofree + 1;        // the answer to a request for a block
   uint64_t* bar_want = bar_clc + 1;         // the producer issued a unit's last load
   uint64_t* bar_drain = bar_want + 1;       // after an abort: the issuer's work landed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + G::NBAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 1);  // (bars + NBAR)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   VUnit* units = reinterpret_cast<VUnit*>(smem + G::OFF_UNIT);
   int* prefix = reinterpret_cast<int*>(smem + G::OFF_PREFIX);

@@ -51,7 +51,7 @@ struct VGeoPP {
   static constexpr int OFF_UNIT = OFF_PREFIX + kSchedChunks * 4;
   static constexpr int OFF_CLC = OFF_UNIT + 2 * 64;
   static constexpr int OFF_BAR = OFF_CLC + 16;
-  static constexpr int NBAR = 2 * NS + 24;
+  static constexpr int NBAR = 2 * NS + 25;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;  // + alignment slack
   static_assert(SMEM <= 232448, "227 KB of shared memory per CTA");
   __device__ static constexpr uint32_t col_s(int t) { return 64u * t; }
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kVppThreads, 1)
   uint64_t* bar_clc = bar_ufree + 2;       // the answer to a request for a block
   uint64_t* bar_want = bar_clc + 1;        // the producer issued a unit's last load
   uint64_t* bar_drain = bar_want + 1;      // after an abort: both issuers' work landed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + G::NBAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_drain + 1);  // (bars + NBAR)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto unit = [&](int k) -> PUnit& { return *reinterpret_cast<PUnit*>(smem + G::OFF_UNIT + (k & 1) * 64); };
 

@@ -210,6 +210,46 @@ def test_decode_two_streams_each_with_its_workspace():
         check_decode(cs[i], qs[i], o, l)
 
 
+def test_captured_behind_a_memset_a_copy_and_another_stream():
+    # what stands before a launch in the graph is no kernel, or comes from two streams
+    zq = _zq()
+    c = Cache([70, 300], 2, 128, 16, "bf16", seed=17)
+    a, q = c.cuda(), _q(2, 8, 128)
+    qd, src = torch.zeros((2, 8, 128), dtype=torch.bfloat16, device="cuda"), q.cuda()
+    out, lse = torch.empty((2, 8, 128), dtype=torch.bfloat16, device="cuda"), torch.empty((2, 8), device="cuda")
+    w = torch.empty(zq.zq_decode_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    kn, vn = (torch.randn((2, 2, 128), generator=torch.Generator().manual_seed(i)).to(torch.bfloat16) for i in (1, 2))
+    kd, vd = kn.cuda(), vn.cuda()
+    have = torch.tensor([69, 299], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    lens = a.pop("cache_seqlens")
+
+    def step():
+        out.zero_()
+        lse.fill_(5.0)
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            zq.kv_append(kd, vd, cache_seqlens=have, **a)
+        qd.copy_(src)
+        main.wait_stream(side)
+        zq.attn_decode(qd, cache_seqlens=lens, out=out, lse=lse, workspace=w, **a)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    out.zero_()
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    for b, pos in ((0, 69), (1, 299)):
+        pg = c.table[b, pos // 16].long()
+        c.store["k"][pg, pos % 16], c.store["v"][pg, pos % 16] = kn[b], vn[b]
+    check_decode(c, q, out, lse)
+
+
 def test_captured_step_follows_the_cache_as_it_grows():
     # append then decode in one graph, replayed while the host advances the lengths
     zq = _zq()

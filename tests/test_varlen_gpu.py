@@ -219,6 +219,25 @@ def test_two_tiles_per_cta_beside_a_sequence_of_nan():
     p.check(out, lse, rows=61, only=(0, 2, 3))
 
 
+def test_two_tiles_per_cta_over_many_sequences():
+    # more sequences than prefix slots, many units per CTA, launches one behind the other
+    p = Pack([(256 + i % 3, 256 + i % 5) for i in range(300)], 8, 2, 128, "bf16", seed=230)
+    a = p.args()
+    assert (a["q"].shape[0] + 255 * 300) // 256 * 8 >= 4 * 148
+    first = _zq().attn_varlen(**a)
+    p.check(*first, only=(0, 1, 149, 150, 298, 299))
+    for got in [_zq().attn_varlen(**a) for _ in range(40)]:
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "leanp"])
+def test_rows_behind_the_last_sequence_cost_nothing_but_time(dtype):
+    # a buffer of 20000 rows of which 300 are in use: the grid is a bound on the buffer
+    p = Pack([(100, 100), (200, 200)], 8, 2, 128, dtype, seed=240, back=19700)
+    out, lse = _zq().attn_varlen(**p.args())
+    p.check(out, lse)
+
+
 def test_no_keys_and_no_queries():
     zq = _zq()
     z = lambda n, h: torch.zeros((n, h, 128), dtype=torch.bfloat16, device="cuda")  # noqa: E731
