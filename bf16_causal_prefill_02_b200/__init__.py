@@ -647,8 +647,8 @@ def attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, out=None, lse=None, softmax
     scale = float(softmax_scale) if softmax_scale else 0.0
 
     def call(s):
-        o = q.new_empty((Tq, Hq, dv), dtype=torch.bfloat16) if out is None else out
-        e = q.new_empty((Hq, Tq), dtype=torch.float32) if lse is None and return_lse else lse
+        o = q.new_empty(Tq, Hq, dv, dtype=torch.bfloat16) if out is None else out
+        e = q.new_empty(Hq, Tq, dtype=torch.float32) if lse is None and return_lse else lse
         a = zq_varlen_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(e), cu_seqlens_q.data_ptr(),
                            cu_seqlens_k.data_ptr(), B, Tq, Tk, Hq, Hkv, dqk, dv, scale, 1 if causal else 0, dtype, qd, kd, vd,
                            int(softmax_mode), 1 if block_scale else 0, int(headroom_T), _ptr(status), layout)
@@ -681,8 +681,8 @@ def _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale
     else:
         raise TypeError("k_cache and v_cache must both be bfloat16 or both FP8 e4m3")
     pages, page_size, Hkv, dqk = kshape
-    dv = vshape[3]
-    if vshape[:3] != kshape[:3]:
+    vpages, vpage_size, vHkv, dv = vshape
+    if vpages != pages or vpage_size != page_size or vHkv != Hkv:
         raise ValueError("v_cache must have k_cache's pages, page size and heads %s, got %s"
                          % (tuple(k_cache.shape[:3]), tuple(v_cache.shape[:3])))
     if block_table.dim() != 2 or block_table.dtype != torch.int32:
@@ -764,8 +764,8 @@ def attn_decode(q, k_cache, v_cache, block_table, cache_seqlens, out=None, lse=N
     scale = float(softmax_scale) if softmax_scale else 0.0
 
     def call(s):
-        o = q.new_empty((B, Hq, dv)) if out is None else out
-        e = q.new_empty((B, Hq), dtype=torch.float32) if lse is None and return_lse else lse
+        o = q.new_empty(B, Hq, dv) if out is None else out
+        e = q.new_empty(B, Hq, dtype=torch.float32) if lse is None and return_lse else lse
         w = q.new_empty(nbytes, dtype=torch.uint8) if workspace is None else workspace
         _check(zq_attn_decode(c, q.data_ptr(), qs, Hq, scale, o.data_ptr(), _ptr(e), w.data_ptr(), s), "zq_attn_decode")
         return o, e

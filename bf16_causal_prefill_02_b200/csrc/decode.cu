@@ -71,6 +71,7 @@ struct DecodeParams {
   // where by_item, else one per entry [piece][team], of the one it begins
   int4* cut;
   int by_item;
+  int whole;     // every (sequence, head tile) is one warp's: no line, no parts
   float* part;   // [piece][team][2][slot]: slot 0 a segment begun by an earlier piece, slot 1 one left to later pieces
 };
 
@@ -137,11 +138,11 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
     return n > 0 ? (int64_t)((n + G::KEYS - 1) / G::KEYS + kSegmentCost) * heads : 0;
   };
   int64_t x = 0, x1 = 0, line = 0;  // this warp's piece
-  int pieces;
+  int pieces = 0;
   const int per_cta = WARPS / p.team;
   const int piece = warp / p.team * gridDim.x + blockIdx.x;  // (few pieces are spread over the SMs)
   const int mine_at = piece * p.team + warp % p.team;        // this warp's entry of cut and part
-  {
+  if (!p.whole) {
     const int per = (c.B + THREADS - 1) / THREADS;
     const int b0 = min((int)threadIdx.x * per, c.B), b1 = min(b0 + per, c.B);
     int64_t mine = 0;
@@ -205,21 +206,32 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
 
   int b = x < x1 ? first_b[warp / p.team] : 0;
   int64_t off = x < x1 ? first_off[warp / p.team] : 0;
-  while (x < x1) {
+  const int flat = c.Hkv * p.head_tiles, stride = gridDim.x * WARPS;
+  int64_t item = blockIdx.x + (int64_t)warp * gridDim.x;  // whole: (sequence, flat head tile)
+  while (p.whole ? item < (int64_t)c.B * flat : x < x1) {
+    if (p.whole) b = (int)(item / flat);
     const int len = keys_of(c, b);
     const int tiles = (len + G::KEYS - 1) / G::KEYS, span = tiles + kSegmentCost;
-    if (len == 0 || off >= (int64_t)span * heads) {
-      off -= len == 0 ? 0 : (int64_t)span * heads;
-      ++b;
-      continue;
+    int fh, t0 = 0, steps = tiles;
+    int64_t start = 0;
+    if (p.whole) {
+      fh = (int)(item % flat);
+      item += stride;
+    } else {
+      if (len == 0 || off >= (int64_t)span * heads) {
+        off -= len == 0 ? 0 : (int64_t)span * heads;
+        ++b;
+        continue;
+      }
+      fh = (int)(off / span) * p.team + warp % p.team;
+      const int r0 = (int)(off % span);
+      const int r1 = (int)min((int64_t)span, r0 + (x1 - x));
+      start = x - r0;  // the (sequence, team)'s first place
+      x += r1 - r0;
+      off += r1 - r0;
+      t0 = max(r0 - kSegmentCost, 0);
+      steps = r1 - kSegmentCost - t0;
     }
-    const int fh = (int)(off / span) * p.team + warp % p.team, r0 = (int)(off % span);
-    const int r1 = (int)min((int64_t)span, r0 + (x1 - x));
-    const int64_t start = x - r0;  // the (sequence, team)'s first place
-    x += r1 - r0;
-    off += r1 - r0;
-    const int t0 = max(r0 - kSegmentCost, 0);
-    const int steps = r1 - kSegmentCost - t0;
     if (steps <= 0) continue;
     const int g = fh / p.head_tiles, ht = fh % p.head_tiles;
     const int h0 = g * p.group + ht * kMaxHeads;            // first query head of the tile
@@ -566,7 +578,7 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
       }
       __syncwarp();
     }
-    if (begins) {
+    if (begins && !p.whole) {
       // its parts: this piece's and those up to the one of its last place.
       // The piece of place y is the largest j with floor(line * j / pieces) <= y.
       const int64_t j = ((start + span) * pieces - 1) / line;
@@ -577,7 +589,7 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
         p.cut[b * c.Hkv * p.head_tiles + fh] = mine;
     }
   }
-  if (!p.by_item && lane == 0) p.cut[mine_at] = cut;
+  if (!p.by_item && !p.whole && lane == 0) p.cut[mine_at] = cut;
 }
 
 // Running (m, l, O) of a row, a lane's four channels of O.
@@ -704,7 +716,7 @@ cudaError_t launch_kernel(DecodeParams& p, cudaStream_t st, int num_sms) {
   p.slot = NT * kHeads * (G::DV + 2);
   // one piece per warp of the CTAs that are resident at once
   constexpr int most = kMaxEntries / G::WARPS;
-  const int grid = num_sms * kCtasPerSm < most ? num_sms * kCtasPerSm : most;
+  int grid = num_sms * kCtasPerSm < most ? num_sms * kCtasPerSm : most;
   const int entries = grid * G::WARPS;
   const int64_t items = (int64_t)p.c.B * p.c.Hkv * p.head_tiles;
   // Blocks of a (sequence, head tile) each where there are few, which then have
@@ -713,11 +725,23 @@ cudaError_t launch_kernel(DecodeParams& p, cudaStream_t st, int num_sms) {
   // blocks, 11.4 / 9.9 and 86 x 1000 keys, 2752 blocks, 70 / 61).
   const int rows = p.group < kMaxHeads ? p.group : kMaxHeads;
   p.by_item = items * rows <= 4 * num_sms && items <= entries ? 1 : 0;
+  // A table with room for few tiles: a warp takes a (sequence, head tile) whole
+  // and there is nothing to join.  Us, split / whole, 32/8 heads: one sequence of
+  // 64 keys bf16 7.5 / 5.8, 128 8.0 / 7.8, 256 8.0 / 12.3; 16 of 256 12.8 / 12.6;
+  // 64 of 256 16.3 / 14.8; e4m3 (32 keys a tile) 1 of 256 8.8 / 9.2.  16/1 heads
+  // have twice the work per tile: 16 of 64 keys 9.7 / 9.0, of 128 10.3 / 11.7.
+  const int whole_tiles = (items >= 128 ? 16 : 8) / NT;
+  p.whole = ((int64_t)p.c.table_width << p.c.page_shift) <= whole_tiles * G::KEYS ? 1 : 0;
+  if (p.whole) {
+    p.by_item = 0;
+    if (items < grid) grid = (int)items;
+  }
   auto kern = decode_kernel<DQK, FP8, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
   if (e != cudaSuccess) return e;
   e = launch_overlapped(kern, dim3((unsigned)grid), dim3(G::THREADS), G::SMEM, st, p);
   if (e != cudaSuccess) return e;
+  if (p.whole) return cudaSuccess;
   if (p.by_item)
     return launch_overlapped(decode_join_kernel<1>, dim3((unsigned)items, (unsigned)rows), dim3(kItemWarps * 32), 0, st, p, entries);
   const unsigned blocks = (unsigned)((entries + kJoinWarps - 1) / kJoinWarps);

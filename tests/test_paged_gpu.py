@@ -113,6 +113,31 @@ def test_decode_splits_and_joins(dtype, lens):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hkv,dqk,page", [(8, 2, 128, 16), (40, 2, 128, 64), (16, 16, 192, 1), (6, 3, 192, 16)])
+def test_decode_small_tables_take_a_warp_per_sequence(dtype, hq, hkv, dqk, page):
+    # at most 4 (16 heads) or 8 tiles of 16 keys: nothing is split
+    lens = [0, 1, 15, 16, 17, 31, 33, 48, 0, 47]
+    c = Cache(lens, hkv, dqk, page, dtype, seed=18)
+    assert (c.table.shape[1] - (page > 1)) * page <= 64  # (the table has a column to spare)
+    a = c.cuda()
+    a["block_table"] = a["block_table"][:, :max(1, 64 // page)].contiguous()
+    q = _q(len(lens), hq, dqk)
+    out, lse = _zq().attn_decode(q.cuda(), **a)
+    check_decode(c, q, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,hq,hkv", [([300] * 200, 8, 2), ([600 + 37 * (i % 9) for i in range(40)], 32, 8), ([5000] + [20] * 150, 16, 4)])
+def test_decode_joins_by_entry(dtype, lens, hq, hkv):
+    # more than 592 (sequence, head) rows: the join goes over the warps' cuts
+    assert len(lens) * hq > 4 * 148
+    c = Cache(lens, hkv, 128, 32, dtype, seed=19)
+    q = _q(len(lens), hq, 128)
+    out, lse = _zq().attn_decode(q.cuda(), **c.cuda())
+    check_decode(c, q, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_decode_more_sequences_than_threads(dtype):
     lens = [(7 * i) % 41 for i in range(777)]
     c = Cache(lens, 1, 128, 16, dtype, seed=9)
