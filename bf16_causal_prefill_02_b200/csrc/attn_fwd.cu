@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Evaluates the software exp2 (degree 3 or 4), CUDA's exp2f (degree 0) or
+// Evaluates the software exp2 (degree 3, 4 or 5), CUDA's exp2f (degree 0) or
 // the MUFU ex2.approx (degree -1) elementwise, for the test of the polynomial.
 __global__ void exp2_check_kernel(const float* __restrict__ x, float* __restrict__ y, int64_t n,
                                   int degree) {
@@ -787,6 +787,8 @@ __global__ void exp2_check_kernel(const float* __restrict__ x, float* __restrict
     exp2_poly_x2<3>(r0, r1, a, b);
   } else if (degree == 4) {
     exp2_poly_x2<4>(r0, r1, a, b);
+  } else if (degree == 5) {
+    exp2_poly_x2<5>(r0, r1, a, b);
   } else if (degree == 0) {
     r0 = exp2f(a);
     r1 = exp2f(b);

@@ -42,7 +42,8 @@ __device__ __forceinline__ void ffma2(float& r0, float& r1, float a0, float a1, 
 // style reduction z = n + f with n = rne(z) (magic-constant add) and
 // f in [-1/2, 1/2], a minimax polynomial p(f) ~ 2^f fitted by the Remez
 // exchange (bf16_causal_prefill_02_b200/csrc/exp2_poly_fit.py; max relative
-// error 7.5e-5 for degree 3, 2.7e-6 for degree 4), and 2^n applied by adding
+// error 7.5e-5 for degree 3, 2.7e-6 for degree 4, 2.3e-7 for degree 5), and
+// 2^n applied by adding
 // n to the exponent bits.  z is clamped at -126 first (results below 2^-126
 // are irrelevant here: they round to 0 in e4m3 and vanish against the row
 // sum in bf16).
@@ -65,6 +66,14 @@ __device__ __forceinline__ void exp2_poly_x2(float& r0, float& r1, float z0, flo
         "fma.rn.f32x2 p, p, f, c;\n\tmov.b64 {%0, %1}, p;\n\t}"
         : "+f"(p0), "+f"(p1)
         : "f"(f0), "f"(f1), "f"(6.932609677e-01f), "f"(9.999280572e-01f));
+  } else if constexpr (DEG == 5) {
+    ffma2(p0, p1, f0, f1, 1.327647245e-03f, 9.675540961e-03f);
+    asm("{\n\t.reg .b64 p, f, c;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 f, {%2, %3};\n\t"
+        "mov.b64 c, {%4, %4};\n\tfma.rn.f32x2 p, p, f, c;\n\tmov.b64 c, {%5, %5};\n\t"
+        "fma.rn.f32x2 p, p, f, c;\n\tmov.b64 c, {%6, %6};\n\tfma.rn.f32x2 p, p, f, c;\n\t"
+        "mov.b64 c, {%7, %7};\n\tfma.rn.f32x2 p, p, f, c;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(p0), "+f"(p1)
+        : "f"(f0), "f"(f1), "f"(5.550713092e-02f), "f"(2.402212024e-01f), "f"(6.931469440e-01f), "f"(1.000000119e+00f));
   } else {
     ffma2(p0, p1, f0, f1, 9.570102207e-03f, 5.591785908e-02f);
     asm("{\n\t.reg .b64 p, f, c;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 f, {%2, %3};\n\t"

@@ -462,13 +462,13 @@ __global__ void __launch_bounds__(kVarThreads, 1)
       float yref = -INFINITY;  // BF16 / running mode: log2-domain reference
       int eref = kInvalidExp;  // FP8: reference exponent
       float l = 0.0f;          // BF16: this thread's half of the row sum
-      float c = p.softmax_scale * 1.4426950408889634f, vscale = 1.0f;
+      float c = p.scale_log2, vscale = 1.0f;
       if (DT == 1) {
         const int di = p.descale_per_kv ? w.b * p.Hkv + w.h / p.group : 0;
         const float qds = p.q_descale ? p.q_descale[di] : 1.0f;
         const float kds = p.k_descale ? p.k_descale[di] : 1.0f;
         vscale = p.v_descale ? p.v_descale[di] : 1.0f;
-        c = ((p.softmax_scale * qds) * kds) * 1.4426950408889634f;
+        c = (p.scale_log2 * qds) * kds;
       }
       for (int j = 0; ok && j < n_kv; ++j) {
         const int x = jt + j, buf = x & 1;
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
               ffma2(z0, z1, s[cc], s[cc + 1], c, ne);
               ffma2(z2, z3, s[cc + 2], s[cc + 3], c, ne);
               if ((cc & 4) == 0) {
-                exp2_poly_x2<4>(p0, p1, z0, z1);
+                exp2_poly_x2<5>(p0, p1, z0, z1);  // (an error near fp32's moves fewest values across a rounding border)
               } else {
                 p0 = ex2_approx(z0);
                 p1 = ex2_approx(z1);

@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kVppThreads, 1)
     const int row = qd * 32 + lane;  // row of the team's tile == TMEM lane
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
     const uint32_t tS = tbase + lane_off + G::col_s(t), tO = tbase + lane_off + G::col_o(t);
-    const float c = p.softmax_scale * 1.4426950408889634f;
+    const float c = p.scale_log2;
     bool ok = true;
     int jt = 0, nq = 0;
 

@@ -61,7 +61,7 @@ struct DecodeParams {
   int64_t q_stride;
   __nv_bfloat16* out;
   float* lse;
-  float scale;
+  float scale;   // softmax scale times log2(e)
   int Hq, group, head_tiles;
   int team;      // warps that walk the same keys of adjacent heads: 1, 2 or 4, dividing the flat head tiles
   int slot;      // floats of a part: O of 8 or 16 heads, then their (m, l)
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
     // ---- queries as B fragments: column (head) quad of each product, and the
     // score scale of the columns 2 ql, 2 ql + 1 that this lane holds of S^T
     uint32_t qb[NT][G::QK_STEPS][2];
-    const float c2 = p.scale * (FP8 && c.k_descale ? c.k_descale[c.descale_per_head ? g : 0] : 1.0f) * 1.4426950408889634f;
+    const float c2 = p.scale * (FP8 && c.k_descale ? c.k_descale[c.descale_per_head ? g : 0] : 1.0f);
     float cr[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -766,7 +766,7 @@ cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t st, int num_sms) {
   p.q_stride = a.q_stride;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
-  p.scale = a.softmax_scale;
+  p.scale = a.scale_log2;
   p.Hq = a.Hq;
   p.group = a.Hq / a.c.Hkv;
   p.head_tiles = (p.group + kMaxHeads - 1) / kMaxHeads;

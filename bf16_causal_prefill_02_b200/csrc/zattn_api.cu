@@ -77,6 +77,11 @@ int validate_attn(const zq_attn_args* a) {
   return ZQ_OK;
 }
 
+// The score scale in the log2 domain (softmax_scale <= 0: 1/sqrt(d_qk)), rounded once.
+float scale_log2(float softmax_scale, int d_qk) {
+  return (float)((softmax_scale > 0.0f ? (double)softmax_scale : 1.0 / std::sqrt((double)d_qk)) * 1.4426950408889634);
+}
+
 }  // namespace
 
 extern "C" {
@@ -401,7 +406,7 @@ int zq_attn_varlen_fwd(const zq_varlen_args* a, void* stream) {
   p.head_group = zq::choose_varlen_head_group(a->Hq, a->Hkv, a->total_k, a->d_qk, a->d_v, fp8 ? 1 : 2);
   p.causal = a->causal ? 1 : 0;
   p.headroom_T = fp8 ? a->headroom_T : 8;
-  p.softmax_scale = a->softmax_scale > 0.0f ? a->softmax_scale : (float)(1.0 / std::sqrt((double)a->d_qk));
+  p.scale_log2 = scale_log2(a->softmax_scale, a->d_qk);
   p.timeout_ns = kTimeoutNs;
   cudaError_t e = zq::launch_attention_varlen(L, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ZQ_OK : ZQ_ERR_CUDA;
@@ -488,7 +493,7 @@ int zq_attn_decode(const zq_paged_kv* cache, const void* q, int64_t q_stride, in
   L.q = q;
   L.q_stride = qs;
   L.Hq = Hq;
-  L.softmax_scale = softmax_scale > 0.0f ? softmax_scale : (float)(1.0 / std::sqrt((double)cache->d_qk));
+  L.scale_log2 = scale_log2(softmax_scale, cache->d_qk);
   L.out = out;
   L.lse = lse;
   L.workspace = workspace;
@@ -499,7 +504,7 @@ int zq_attn_decode(const zq_paged_kv* cache, const void* q, int64_t q_stride, in
 int zq_debug_exp2(const float* x, float* y, int64_t n, int degree, void* stream) {
   if (n < 0) return ZQ_ERR_SHAPE;
   if (n > 0 && (!x || !y)) return ZQ_ERR_NULL;
-  if (degree != 3 && degree != 4 && degree != 0 && degree != -1) return ZQ_ERR_UNSUPPORTED;
+  if (degree != 3 && degree != 4 && degree != 5 && degree != 0 && degree != -1) return ZQ_ERR_UNSUPPORTED;
   int rc = check_device(nullptr);
   if (rc != ZQ_OK) return rc;
   cudaError_t e = zq::launch_exp2_check(x, y, n, degree, static_cast<cudaStream_t>(stream));

@@ -122,7 +122,7 @@ struct VarlenParams {
   int head_group;  // query heads whose units are interleaved; divides Hq
   int causal;
   int headroom_T;
-  float softmax_scale;
+  float scale_log2;  // softmax scale times log2(e)
   uint64_t timeout_ns;
 };
 struct VarlenLaunch {
@@ -167,7 +167,7 @@ struct DecodeLaunch {
   const void* q;
   int64_t q_stride;  // elements between sequences
   int Hq;
-  float softmax_scale;
+  float scale_log2;
   void* out;
   float* lse;
   void* workspace;

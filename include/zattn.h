@@ -487,8 +487,8 @@ ZQ_API int zq_attn_decode(const zq_paged_kv* cache, const void* q, int64_t q_str
 /* Bytes of device scratch zq_attn_decode needs (a constant, about 21 MB). */
 ZQ_API size_t zq_decode_workspace_bytes(void);
 
-/* zq_debug_exp2 -- y[i] = 2^x[i] by the kernels' software exp2 (degree 3 or
- * 4 minimax polynomial after range reduction), by CUDA's exp2f (degree 0) or
+/* zq_debug_exp2 -- y[i] = 2^x[i] by the kernels' software exp2 (degree 3, 4
+ * or 5 minimax polynomial after range reduction), by CUDA's exp2f (degree 0) or
  * by the hardware approximation ex2.approx (degree -1).  x, y: device fp32
  * arrays of n elements.  For the test that bounds the polynomial's error
  * against exp2f.  Errors: ZQ_ERR_SHAPE, ZQ_ERR_NULL, ZQ_ERR_UNSUPPORTED,

@@ -201,6 +201,35 @@ def test_decode_e4m3_takes_queries_of_any_size():
         assert ((lse.double().cpu() - rl).abs() <= 2.0 ** -10 + 2.0 ** -22 * rl.abs())[:, h].all(), h
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_offsets_past_32_bits(dtype):
+    # pages at the end of caches of more than 2^31 elements
+    zq = _zq()
+    c = Cache([100, 37], 8, 128, 64, dtype, seed=21, waste=None)
+    pages = 33000
+    assert pages * 64 * 8 * 128 > 2 ** 31
+    a = c.cuda()
+    for x in "kv":
+        big = torch.empty((pages, 64, 8, 128), dtype=a[x + "_cache"].dtype, device="cuda")
+        big[pages - c.pages:].view(torch.uint8).copy_(a[x + "_cache"].view(torch.uint8))
+        a[x + "_cache"] = big
+    a["block_table"] += (a["block_table"] >= 0).int() * (pages - c.pages)
+    q = _q(2, 32, 128)
+    out, lse = zq.attn_decode(q.cuda(), **a)
+    check_decode(c, q, out, lse)
+    kn, vn = (torch.randn((2, 8, 128), generator=torch.Generator().manual_seed(i)).to(torch.bfloat16) for i in (3, 4))
+    lens = a.pop("cache_seqlens")
+    zq.kv_append(kn.cuda(), vn.cuda(), cache_seqlens=lens - 1, **a)
+    out, lse = zq.attn_decode(q.cuda(), cache_seqlens=lens, **a)
+    c.store = {x: a[x + "_cache"][pages - c.pages:].cpu() for x in "kv"}
+    for b in range(2):  # the last key is the new one
+        n = c.lens[b] - 1
+        got = c.rows("k", b)[0][n] / (c.descale["k"].double()[:, None] if dtype == "e4m3" else 1.0)
+        want = kn[b] if dtype == "bf16" else (kn[b].float() * (1.0 / c.descale["k"])[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+        assert (got - want.double()).abs().max().item() <= 1e-9 * 448
+    check_decode(c, q, out, lse)
+
+
 def test_decode_nan_and_infinity_in_visible_keys_show():
     c = Cache([40, 40], 1, 128, 16, "bf16", seed=14)
     c.store["k"][c.table[0, 1].long(), 3, 0, 5] = float("nan")

@@ -176,7 +176,9 @@ def test_growing_logits_move_the_reference(dtype):
 
 @pytest.mark.parametrize("dtype", ["exact", "leanp"])
 @pytest.mark.parametrize("dqk", [128, 192])
-def test_fp8_equals_the_fixed_batch_kernel_bit_for_bit(dtype, dqk):
+def test_fp8_agrees_with_the_fixed_batch_kernel(dtype, dqk):
+    # the same P but for keys next to a rounding border (another order of the
+    # scale's factors, a closer exp2): a row differs by at most one code step
     zq = _zq()
     c = Case(2, 700, 700, 4, 2, dqk, 128, dtype=dtype, seed=7)
     o, l = c.run_gpu()
@@ -185,8 +187,20 @@ def test_fp8_equals_the_fixed_batch_kernel_bit_for_bit(dtype, dqk):
     cu = torch.tensor([0, 700, 1400], dtype=torch.int32, device="cuda")
     mode = zq.ZQ_SOFTMAX_EXACT if dtype == "exact" else zq.ZQ_SOFTMAX_LEANP
     ov, lv = zq.attn_varlen(q, k, v, cu, cu, softmax_mode=mode, **ds)
-    assert torch.equal(ov.view(2, 700, 4, 128), o)
-    assert torch.equal(lv.view(4, 2, 700).transpose(0, 1), l)
+    assert (lv.view(4, 2, 700).transpose(0, 1) - l).abs().max().item() <= LSE_FLIP_BOUND[dtype]
+    assert (ov.view(2, 700, 4, 128).float() - o.float()).abs().max().item() <= CODE_STEP[dtype] * 2 * np.abs(c.vd).max()
+    assert (ov.view(2, 700, 4, 128) != o).any(dim=-1).float().mean().item() <= 0.05
+
+
+@pytest.mark.parametrize("lo,hi", [(-0.5, 0.5), (-100.0, 0.0)])
+def test_degree_5_exp2(lo, hi):
+    # fitted bound 2.33e-7 in fp32 Horner, one further rounding for the fused steps' order and the reference's own
+    zq = _zq()
+    x = torch.linspace(lo, hi, 100001, device="cuda")
+    y = torch.empty_like(x)
+    assert zq.zq_debug_exp2(x.data_ptr(), y.data_ptr(), x.numel(), 5, torch.cuda.current_stream().cuda_stream) == zq.ZQ_OK
+    rel = (y.double() / torch.exp2(x.double()) - 1).abs().max().item()
+    assert rel <= 2.33e-7 + 2.0 ** -23, rel
 
 
 # At least 4 x 148 units of 256 rows and 256 rows a sequence: two query tiles
@@ -236,6 +250,20 @@ def test_rows_behind_the_last_sequence_cost_nothing_but_time(dtype):
     p = Pack([(100, 100), (200, 200)], 8, 2, 128, dtype, seed=240, back=19700)
     out, lse = _zq().attn_varlen(**p.args())
     p.check(out, lse)
+
+
+@pytest.mark.parametrize("hq", [64, 2])
+def test_rows_past_32_bits(hq):
+    # the last rows of a query tensor of more than 2^31 elements (both kernels: two tiles per CTA with 64 heads)
+    p = Pack([(300, 300)], hq, 2, 128, "bf16", seed=250)
+    a = p.args()
+    rows = 2 ** 31 // (64 * 128) + 500
+    big = torch.empty((rows, hq, 128), dtype=torch.bfloat16, device="cuda")
+    big[rows - 300:] = a["q"]
+    out = torch.empty_like(big)
+    cu = torch.tensor([rows - 300, rows], dtype=torch.int32, device="cuda")
+    _, lse = _zq().attn_varlen(big, a["k"], a["v"], cu, a["cu_seqlens_k"], out=out)
+    p.check(out[rows - 300:], lse[:, rows - 300:])
 
 
 def test_no_keys_and_no_queries():
