@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
       if (y < at0 || y >= at0 + mine) continue;
       int64_t at = at0;
       int b = b0;
-      for (;; ++b) {
+      for (; b + 1 < b1; ++b) {
         const int64_t n = places(b);
         if (y < at + n) break;
         at += n;
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
     } else {
       if (len == 0 || off >= (int64_t)span * heads) {
         off -= len == 0 ? 0 : (int64_t)span * heads;
-        ++b;
+        if (++b >= c.B) break;
         continue;
       }
       fh = (int)(off / span) * p.team + warp % p.team;
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
     if (begins && !p.whole) {
       // its parts: this piece's and those up to the one of its last place.
       // The piece of place y is the largest j with floor(line * j / pieces) <= y.
-      const int64_t j = ((start + span) * pieces - 1) / line;
+      const int64_t j = min(((start + span) * pieces - 1) / line, (int64_t)pieces - 1);
       const int4 mine = make_int4(b, fh, ends ? 0 : (int)(j - piece) + 1, mine_at);
       if (!p.by_item)
         cut = ends ? cut : mine;
