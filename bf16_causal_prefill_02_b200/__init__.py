@@ -13,8 +13,8 @@ a stream handle).  The torch-level helpers ``attn_fwd``, ``quantize_fp8``,
 marshal tensors into those calls; ``attn_plan``
 returns the schedule of a call (host only).  ``attn_varlen`` and
 ``flash_attn_varlen_func`` take packed prompts of different lengths;
-``kv_append`` and ``attn_decode`` carry on where the prompt ends: new keys and values into a paged cache, and
-attention of one new token over it.
+``kv_append`` and ``attn_decode`` carry on where the prompt ends: new keys and
+values into a paged cache, and attention of one new token over it.
 """
 from __future__ import annotations
 

@@ -450,7 +450,9 @@ typedef struct zq_paged_kv {
  * cache_seqlens is read, not advanced.  Tokens of no sequence, and tokens
  * whose position lies past the table or on a page outside [0, num_pages), are
  * dropped.  Two tokens that the table sends to the same place are the
- * caller's error: that place then holds parts of either.
+ * caller's error: that place then holds parts of either.  Offsets that do not
+ * ascend leave open which sequence a token goes to, or whether it is dropped;
+ * nothing outside the cache's pages is written.
  * T == 0 does nothing (k, v may then be NULL).
  * Errors: ZQ_ERR_NULL, ZQ_ERR_SHAPE (sizes <= 0, T < 0 or != B without
  *   cu_seqlens, a stride too small, page_size no power of two, products past
@@ -476,9 +478,10 @@ ZQ_API int zq_kv_append(const zq_paged_kv* cache, const void* k, const void* v, 
  *        used by another call that runs at the same time.
  * A sequence without keys (length 0, or no key on a page of the cache) gets
  * out = 0, lse = -inf.  Rows past a sequence's length are not read.  e4m3
- * codes enter the products exactly (as f16); the weights are rounded to bf16
- * (bf16 caches) or f16 (e4m3 caches), sums are fp32.
- * Two stream operations (two kernels).  Runs repeat bit for bit.
+ * codes enter the products exactly (as f16); the weights enter as the sum of
+ * two bf16 values (bf16 caches) or rounded to f16 (e4m3 caches), sums are
+ * fp32.  One stream operation where the table has room for few keys, else two
+ * (kernels).  Runs repeat bit for bit.
  * Errors: as zq_kv_append, with q, out, lse and workspace.
  */
 ZQ_API int zq_attn_decode(const zq_paged_kv* cache, const void* q, int64_t q_stride, int Hq,
