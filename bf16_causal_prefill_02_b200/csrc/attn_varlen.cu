@@ -619,18 +619,12 @@ __global__ void __launch_bounds__(kVarThreads, 1)
       const bool empty = L == 0.0f || (DT == 0 && yref == -INFINITY && L == L);
       const float inv = empty ? 0.0f : vscale / L;
       if (!empty) lse_v = ((DT == 0 ? yref : (float)eref) + __log2f(L)) * 0.6931471805599453f;
-      if (row < w.rows) {
-        const int64_t i = (int64_t)w.q_row + row;
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (i * p.Hq + w.h) * DV + col_h);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float f[8];
-#pragma unroll
-          for (int z = 0; z < 8; ++z) f[z] = empty ? 0.0f : __uint_as_float(o[8 * q + z]) * inv;
-          dst[q] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-        }
-        if (half == 0 && p.lse) p.lse[(int64_t)w.h * p.Tq + i] = lse_v;
-      }
+      const int row4 = row & ~3;
+      const int64_t stride = (int64_t)p.Hq * DV;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)w.q_row + row4) * stride + w.h * DV + col_h;
+      store_channels<0>(dst, stride, w.rows - row4, o, inv, empty, lane);
+      store_channels<32>(dst + 32, stride, w.rows - row4, o, inv, empty, lane);
+      if (row < w.rows && half == 0 && p.lse) p.lse[(int64_t)w.h * p.Tq + w.q_row + row] = lse_v;
       // the unit is done: its slot may name the unit after next
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_ufree + (k & 1));

@@ -430,8 +430,9 @@ __global__ void __launch_bounds__(kVppThreads, 1)
         inv = empty ? 0.0f : 1.0f / l;
         if (!empty) lse_v = (yref + __log2f(l)) * 0.6931471805599453f;
       }
-      const int64_t i = (int64_t)q_row + row;
-      __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + (i * p.Hq + h) * G::D;
+      const int row4 = row & ~3;
+      const int64_t stride = (int64_t)p.Hq * G::D;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)q_row + row4) * stride + h * G::D;
 #pragma unroll 1
       for (int ch = 0; ch < 2; ++ch) {
         uint32_t o[64];
@@ -446,18 +447,10 @@ __global__ void __launch_bounds__(kVppThreads, 1)
           tc_fence_before();
           mbar_arrive(bar_ofree + t);  // O_t read: the next unit's PV_t(0) may overwrite it
         }
-        if (row < rows) {
-          uint4* dst = reinterpret_cast<uint4*>(orow + ch * 64);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            float f[8];
-#pragma unroll
-            for (int z = 0; z < 8; ++z) f[z] = empty ? 0.0f : __uint_as_float(o[8 * q + z]) * inv;
-            dst[q] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-          }
-        }
+        store_channels<0>(dst + ch * 64, stride, rows - row4, o, inv, empty, lane);
+        store_channels<32>(dst + ch * 64 + 32, stride, rows - row4, o, inv, empty, lane);
       }
-      if (row < rows && p.lse) p.lse[(int64_t)h * p.Tq + i] = lse_v;
+      if (row < rows && p.lse) p.lse[(int64_t)h * p.Tq + q_row + row] = lse_v;
       // the unit is done: its slot may name the unit after next
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_ufree + (k & 1));

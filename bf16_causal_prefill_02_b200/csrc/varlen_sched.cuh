@@ -11,9 +11,12 @@
 // with a long unit does not hold a second one that an idle CTA could run
 // (8192 rows, 4 heads: 91 against 125 us when asked a whole unit ahead),
 // early enough for the answer to hide behind the stages still to be consumed.
+//
+// And how they write their output rows (store_channels).
 #pragma once
 #include <cstdint>
 
+#include "attn_math.cuh"
 #include "sm100_ptx.cuh"
 #include "zq_internal.h"
 
@@ -170,6 +173,55 @@ __device__ __forceinline__ bool schedule_units(const VarlenParams& p, int heads,
     __syncwarp();
     if (last) return true;
   }
+}
+
+// Transposes 4 x 4 pieces of 16 bytes over each four lanes: v[j] of lane i
+// becomes v[i] of lane j.
+__device__ __forceinline__ void transpose_pieces(uint4 (&v)[4], int lane) {
+#pragma unroll
+  for (int b = 1; b < 4; b <<= 1) {
+    const bool hi = lane & b;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & b) continue;
+      uint4 s = hi ? v[j] : v[j | b];
+      s.x = __shfl_xor_sync(0xffffffffu, s.x, b);
+      s.y = __shfl_xor_sync(0xffffffffu, s.y, b);
+      s.z = __shfl_xor_sync(0xffffffffu, s.z, b);
+      s.w = __shfl_xor_sync(0xffffffffu, s.w, b);
+      if (hi)
+        v[j] = s;
+      else
+        v[j | b] = s;
+    }
+  }
+}
+
+// Writes 32 channels of an output row per lane, o[OFF ..] scaled by inv (0
+// where `empty`), as bf16.  Four adjacent lanes hold four adjacent rows and
+// exchange pieces first, so that they write 64 bytes of one row together, not
+// half a sector of a row each.  `out`: the first of the channels in the first
+// of the four rows, `rows` (0 or less: none) of which are written, `stride`
+// elements apart.  Each lane its own row / with the exchange (us): one tile per
+// CTA, 32/8 heads 1024 rows bf16 19.1 / 17.8, 192/128 351 / 344, FP8 exact
+// 346 / 334, Lean P 272 / 267; two tiles, 12 prompts 288 / 285, 16384 rows
+// 1903 / 1869.
+template <int OFF, int N>
+__device__ __forceinline__ void store_channels(__nv_bfloat16* out, int64_t stride, int rows, const uint32_t (&o)[N], float inv, bool empty,
+                                               int lane) {
+  uint4 v[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float f[8];
+#pragma unroll
+    for (int z = 0; z < 8; ++z) f[z] = empty ? 0.0f : __uint_as_float(o[OFF + 8 * q + z]) * inv;
+    v[q] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  }
+  transpose_pieces(v, lane);
+  out += (lane & 3) * 8;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (r < rows) *reinterpret_cast<uint4*>(out + r * stride) = v[r];
 }
 
 }  // namespace zq
