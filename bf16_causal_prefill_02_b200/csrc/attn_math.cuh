@@ -38,6 +38,13 @@ __device__ __forceinline__ void ffma2(float& r0, float& r1, float a0, float a1, 
       : "=f"(r0), "=f"(r1)
       : "f"(a0), "f"(a1), "f"(b), "f"(c));
 }
+// (r0, r1) += (a0, a1)
+__device__ __forceinline__ void fadd2(float& r0, float& r1, float a0, float a1) {
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(r0), "+f"(r1)
+      : "f"(a0), "f"(a1));
+}
 // Software 2^z for a pair of values (offloads the MUFU unit).  Cody-Waite
 // style reduction z = n + f with n = rne(z) (magic-constant add) and
 // f in [-1/2, 1/2], a minimax polynomial p(f) ~ 2^f fitted by the Remez

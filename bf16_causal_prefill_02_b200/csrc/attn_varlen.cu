@@ -509,14 +509,15 @@ __global__ void __launch_bounds__(kVarThreads, 1)
           const float nb = yref == -INFINITY ? 0.0f : -yref;
           uint32_t pk[32];
           float lp0 = 0.0f, lp1 = 0.0f;
-          // A quarter of the pairs runs on the FMA pipe, but not where keys are
-          // masked: the polynomial does not give 0 for them.
+          // A quarter (d_qk = 192: an eighth) of the pairs runs on the FMA pipe,
+          // but not where keys are masked: the polynomial does not give 0 for
+          // them.  (us, 1/4 / 1/8: 4096 rows, 32/8 heads 132 / 134; 192/128 339 / 330)
           auto weights = [&](auto poly) {
 #pragma unroll
             for (int cc = 0; cc < 64; cc += 2) {
               float z0, z1, p0, p1;
               ffma2(z0, z1, s[cc], s[cc + 1], c, nb);
-              if (poly.value && (cc & 6) == 0) {
+              if (poly.value && (cc & (DQK == 128 ? 6 : 14)) == 0) {
                 exp2_poly_x2<kPolyDegree>(p0, p1, z0, z1);
               } else {
                 p0 = ex2_approx(z0);

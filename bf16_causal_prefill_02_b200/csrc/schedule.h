@@ -124,11 +124,11 @@ inline int varlen_tiles(int64_t Tq, int64_t B, int rows) {
 // Packed prompts, BF16 at d = 128: two tiles per CTA (attn_varlen_pp.cu) where
 // there are enough units to keep the SMs even, and sequences long enough to
 // fill both tiles.  Measured against one tile per CTA (us, one / two):
-//   units of 256 rows  192: 33.0 / 34.1   376: 253 / 271   512: 239 / 243
-//   640: 202 / 199     752: 498 / 496     1024: 478 / 468  1952: 146 / 121
-//   41 sequences of 100 rows, 32 heads: 39 / 45.
+//   units of 256 rows  192: 29.8 / 31.9   376: 252 / 257   416: 87 / 90
+//   472: 44.4 / 46.7   512: 237 / 232     640: 197 / 190   1024: 469 / 449
+//   41 sequences of 100 rows, 32 heads: 34.5 / 43.5.
 inline bool use_varlen_pairs(int64_t Tq, int64_t B, int Hq, int num_sms) {
-  return (int64_t)varlen_tiles(Tq, B, 2 * kTile) * Hq >= 4 * (int64_t)num_sms && Tq >= 2 * kTile * B;
+  return 3 * (int64_t)varlen_tiles(Tq, B, 2 * kTile) * Hq >= 10 * (int64_t)num_sms && Tq >= 2 * kTile * B;
 }
 
 // Packed prompts: heads whose units are interleaved.  All of them, which
