@@ -18,6 +18,11 @@
 //     are set to 0 in shared memory before the product, so that what they hold
 //     (infinities and NaN too) does not matter.
 //
+// Bound by the softmax chain of a tile (the tensor pipe is 41-61% busy): after
+// a pause, 16/16 heads 192/128 over 12136 rows 326 us (1174 TFLOP/s), FP8 Lean
+// P, 32/8 heads, 5060 rows in chunks over 19793 keys 268 us (1544), one prompt of
+// 16384 rows 1246 us (1765), bf16 4096 rows 129 us (1066).
+//
 // Warps: 0-7 softmax and epilogue (a 16-lane group of TMEM rows each, threads
 // t and t + 16 share a query row, one 64-key half of the tile each), 8 TMA
 // producer, 9 tcgen05 issuer, 10 scheduler.  Tensor memory as in attn_fwd.cu:

@@ -5,7 +5,7 @@
 // sequence offsets), looks up the page its position falls in, and moves the
 // share of the key and value rows, 16 bytes a lane at a time.  The rows are on
 // their way from memory while the place is looked up.  Bound by memory: 2
-// bytes read and 2 (bf16) or 1 (e4m3) written per element (14827 tokens of 8
+// bytes read and 2 (bf16) or 1 (e4m3) written per element (15739 tokens of 8
 // heads to e4m3, 97 MB: 19.1 us); a step of one token each is bound by the
 // chain of loads (64 sequences: 2.6 us).
 #include "paged.cuh"
