@@ -19,7 +19,8 @@
 //     head) writes the output; a cut one writes (m, l, O) to the workspace and
 //     decode_join_kernel joins the parts: M = max m_j, l = sum l_j 2^(m_j - M),
 //     o = sum O_j 2^(m_j - M) / l.  The order is fixed, so runs repeat bit for
-//     bit.
+//     bit.  Where the table has room for few keys there is no line: the warps of
+//     a block share a (sequence, kv head) and join in shared memory.
 //     Pieces go to warps side by side: where the heads allow it, the 2 or 4
 //     warps of a team walk the same keys of adjacent heads, so that the 256
 //     (bf16) or 128 (e4m3) bytes that a head has of a key are read together
@@ -71,7 +72,7 @@ struct DecodeParams {
   // where by_item, else one per entry [piece][team], of the one it begins
   int4* cut;
   int by_item;
-  int whole;     // every (sequence, head tile) is one warp's: no line, no parts
+  int share;     // without a line: warps that share a (sequence, head tile), 1 or all of the block
   float* part;   // [piece][team][2][slot]: slot 0 a segment begun by an earlier piece, slot 1 one left to later pieces
 };
 
@@ -115,7 +116,25 @@ __device__ __forceinline__ int keys_of(const PagedKV& c, int b) {
   return (int)min((int64_t)max(c.seqlens[b], 0), cap);
 }
 
-template <int DQK, int FP8, int NT>
+// Running (m, l, O) of a row, a lane's four channels of O.
+struct Part {
+  float m = -INFINITY, l = 0.0f;
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  __device__ __forceinline__ void add(float2 st, float4 v) {
+    const float nm = fmaxf(m, st.x), nb = nm == -INFINITY ? 0.0f : nm;
+    const float fa = ex2_approx(m - nb), fb = ex2_approx(st.x - nb);
+    l = l * fa + st.y * fb;
+    a.x = a.x * fa + v.x * fb;
+    a.y = a.y * fa + v.y * fb;
+    a.z = a.z * fa + v.z * fb;
+    a.w = a.w * fa + v.w * fb;
+    m = nm;
+  }
+};
+
+// LINE: the keys as one line in equal pieces, with parts for the join.  Else a
+// (sequence, head tile) is one warp's or one block's, and nothing is left.
+template <int DQK, int FP8, int NT, int LINE>
 __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) decode_kernel(const DecodeParams p) {
   using G = DecGeo<DQK, FP8, NT>;
   constexpr int DV = G::DV, NS = G::NS, WARPS = G::WARPS, THREADS = G::THREADS;
@@ -124,6 +143,7 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
   __shared__ int64_t scan[WARPS];
   __shared__ int64_t first_off[WARPS];
   __shared__ int first_b[WARPS];
+  __shared__ float2 stat_s[WARPS][kMaxHeads];
   const PagedKV& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane >> 2, ql = lane & 3;
@@ -142,7 +162,7 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
   const int per_cta = WARPS / p.team;
   const int piece = warp / p.team * gridDim.x + blockIdx.x;  // (few pieces are spread over the SMs)
   const int mine_at = piece * p.team + warp % p.team;        // this warp's entry of cut and part
-  if (!p.whole) {
+  if constexpr (LINE) {
     const int per = (c.B + THREADS - 1) / THREADS;
     const int b0 = min((int)threadIdx.x * per, c.B), b1 = min(b0 + per, c.B);
     int64_t mine = 0;
@@ -192,7 +212,7 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
   // sequences without keys: 0 and -inf
   for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
     if (keys_of(c, b) > 0) continue;
-    if (p.by_item)
+    if (LINE && p.by_item)
       for (int i = threadIdx.x; i < c.Hkv * p.head_tiles; i += THREADS) p.cut[b * c.Hkv * p.head_tiles + i] = make_int4(0, 0, 0, 0);
     for (int i = threadIdx.x; i < p.Hq * DV / 2; i += THREADS)
       reinterpret_cast<uint32_t*>(p.out + (int64_t)b * p.Hq * DV)[i] = 0u;
@@ -204,19 +224,31 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
   const int64_t krow = (int64_t)c.Hkv * (DQK * G::ES), vrow = (int64_t)c.Hkv * (DV * G::ES);
   int4 cut = make_int4(0, 0, 0, 0);  // the segment of this piece that is left to later ones
 
-  int b = x < x1 ? first_b[warp / p.team] : 0;
-  int64_t off = x < x1 ? first_off[warp / p.team] : 0;
-  const int flat = c.Hkv * p.head_tiles, stride = gridDim.x * WARPS;
-  int64_t item = blockIdx.x + (int64_t)warp * gridDim.x;  // whole: (sequence, flat head tile)
-  while (p.whole ? item < (int64_t)c.B * flat : x < x1) {
-    if (p.whole) b = (int)(item / flat);
+  int b = 0;
+  int64_t off = 0;
+  if (LINE && x < x1) {
+    b = first_b[warp / p.team];
+    off = first_off[warp / p.team];
+  }
+  const int flat = c.Hkv * p.head_tiles;
+  // without a line: items are (sequence, flat head tile)
+  const bool shared = !LINE && p.share > 1;
+  const int64_t items = (int64_t)c.B * flat;
+  int64_t item = shared ? blockIdx.x : blockIdx.x + (int64_t)warp * gridDim.x;
+  while (LINE ? x < x1 : item < items) {
+    if (!LINE) b = (int)(item / flat);
     const int len = keys_of(c, b);
     const int tiles = (len + G::KEYS - 1) / G::KEYS, span = tiles + kSegmentCost;
     int fh, t0 = 0, steps = tiles;
     int64_t start = 0;
-    if (p.whole) {
+    if constexpr (!LINE) {
       fh = (int)(item % flat);
-      item += stride;
+      item += shared ? gridDim.x : (int64_t)gridDim.x * WARPS;
+      if (shared) {  // a part of the keys each
+        t0 = tiles * warp / WARPS;
+        steps = tiles * (warp + 1) / WARPS - t0;
+      }
+      if (len == 0) continue;
     } else {
       if (len == 0 || off >= (int64_t)span * heads) {
         off -= len == 0 ? 0 : (int64_t)span * heads;
@@ -231,8 +263,8 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
       off += r1 - r0;
       t0 = max(r0 - kSegmentCost, 0);
       steps = r1 - kSegmentCost - t0;
+      if (steps <= 0) continue;
     }
-    if (steps <= 0) continue;
     const int g = fh / p.head_tiles, ht = fh % p.head_tiles;
     const int h0 = g * p.group + ht * kMaxHeads;            // first query head of the tile
     const int rows = min(kMaxHeads, p.group - ht * kMaxHeads);  // query heads in it
@@ -530,14 +562,25 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
     cp_async_wait<0>();
     __syncwarp();
 
-    // ---- the segment's end: to the output, or to this piece's slot.  O^T goes
-    // through the ring so that rows of channels are written whole.
+    // ---- the segment's end: to the output, to this piece's slot, or joined
+    // with the other warps' parts.  O^T goes through the ring so that rows of
+    // channels are written whole.
     const bool begins = t0 == 0, ends = t0 + steps == tiles;
     const float vds = FP8 && c.v_descale ? c.v_descale[c.descale_per_head ? g : 0] : 1.0f;
     float* const slot = p.part + ((int64_t)mine_at * 2 + (begins ? 1 : 0)) * p.slot;
-    float* const turn = reinterpret_cast<float*>(smem + warp * G::RING);  // [8 heads][132]
     constexpr int PITCH = DV + 4;
-    static_assert(kHeads * PITCH * 4 <= G::RING, "a product's O fits the ring");
+    static_assert(NT * kHeads * PITCH * 4 <= G::RING, "all O fit the ring");
+    auto turn_of = [&](int w) { return reinterpret_cast<float*>(smem + w * G::RING); };  // [8 or 16 heads][132]
+    float* const turn = turn_of(warp);
+    auto write_row = [&](int h, float m, float sum, float4 v) {
+      const int64_t row = (int64_t)b * p.Hq + h0 + h;
+      // no key was there (sum = 0): 0 and -inf; NaN stays NaN
+      const bool empty = sum == 0.0f;
+      const float inv = vds / sum;
+      reinterpret_cast<uint2*>(p.out + row * DV)[lane] =
+          empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+      if (p.lse && lane == 0) p.lse[row] = empty ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -547,7 +590,7 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
         l[nt][i] += __shfl_xor_sync(kFull, l[nt][i], 16);
 #pragma unroll
         for (int n = 0; n < DV / 16; ++n) {
-          float* dst = turn + (2 * ql + i) * PITCH + n * 16;
+          float* dst = turn + (nt * kHeads + 2 * ql + i) * PITCH + n * 16;
           if constexpr (!FP8) {
             dst[quad] = o[nt][n][i];
             dst[quad + 8] = o[nt][n][2 + i];
@@ -556,21 +599,22 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
           }
         }
       }
+      if (shared) {
+        if (quad == 0) {
+          stat_s[warp][nt * kHeads + 2 * ql] = make_float2(ref[nt][0], l[nt][0]);
+          stat_s[warp][nt * kHeads + 2 * ql + 1] = make_float2(ref[nt][1], l[nt][1]);
+        }
+        continue;
+      }
       __syncwarp();
 #pragma unroll
       for (int r = 0; r < kHeads; ++r) {
         const int h = nt * kHeads + r;
         const float m = __shfl_sync(kFull, ref[nt][r & 1], r >> 1), sum = __shfl_sync(kFull, l[nt][r & 1], r >> 1);
         if (h >= rows) break;
-        const float4 v = *reinterpret_cast<const float4*>(turn + r * PITCH + lane * 4);
-        if (begins && ends) {
-          const int64_t row = (int64_t)b * p.Hq + h0 + h;
-          // no key was there (sum = 0): 0 and -inf; NaN stays NaN
-          const bool empty = sum == 0.0f;
-          const float inv = vds / sum;
-          reinterpret_cast<uint2*>(p.out + row * DV)[lane] =
-              empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
-          if (p.lse && lane == 0) p.lse[row] = empty ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+        const float4 v = *reinterpret_cast<const float4*>(turn + h * PITCH + lane * 4);
+        if (!LINE || (begins && ends)) {
+          write_row(h, m, sum, v);
         } else {
           reinterpret_cast<float4*>(slot + h * DV)[lane] = v;
           if (lane == 0) *reinterpret_cast<float2*>(slot + p.slot - NT * kHeads * 2 + 2 * h) = make_float2(m, sum);
@@ -578,7 +622,17 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
       }
       __syncwarp();
     }
-    if (begins && !p.whole) {
+    if (shared) {
+      __syncthreads();
+      for (int h = warp; h < rows; h += WARPS) {
+        Part all;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) all.add(stat_s[w][h], *reinterpret_cast<const float4*>(turn_of(w) + h * PITCH + lane * 4));
+        write_row(h, all.m, all.l, all.a);
+      }
+      __syncthreads();  // (the rings are loaded again)
+    }
+    if (LINE && begins) {
       // its parts: this piece's and those up to the one of its last place.
       // The piece of place y is the largest j with floor(line * j / pieces) <= y.
       const int64_t j = min(((start + span) * pieces - 1) / line, (int64_t)pieces - 1);
@@ -589,24 +643,8 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
         p.cut[b * c.Hkv * p.head_tiles + fh] = mine;
     }
   }
-  if (!p.by_item && !p.whole && lane == 0) p.cut[mine_at] = cut;
+  if (LINE && !p.by_item && lane == 0) p.cut[mine_at] = cut;
 }
-
-// Running (m, l, O) of a row, a lane's four channels of O.
-struct Part {
-  float m = -INFINITY, l = 0.0f;
-  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  __device__ __forceinline__ void add(float2 st, float4 v) {
-    const float nm = fmaxf(m, st.x), nb = nm == -INFINITY ? 0.0f : nm;
-    const float fa = ex2_approx(m - nb), fb = ex2_approx(st.x - nb);
-    l = l * fa + st.y * fb;
-    a.x = a.x * fa + v.x * fb;
-    a.y = a.y * fa + v.y * fb;
-    a.z = a.z * fa + v.z * fb;
-    a.w = a.w * fa + v.w * fb;
-    m = nm;
-  }
-};
 
 // Joins the parts of what was cut; blockIdx.y is the query head in the head
 // tile.  BY_ITEM: a block for each (sequence, head tile), its warps share the
@@ -725,23 +763,20 @@ cudaError_t launch_kernel(DecodeParams& p, cudaStream_t st, int num_sms) {
   // blocks, 11.4 / 9.9 and 86 x 1000 keys, 2752 blocks, 70 / 61).
   const int rows = p.group < kMaxHeads ? p.group : kMaxHeads;
   p.by_item = items * rows <= 4 * num_sms && items <= entries ? 1 : 0;
-  // A table with room for few tiles: a warp takes a (sequence, head tile) whole
-  // and there is nothing to join.  Us, split / whole, 32/8 heads: one sequence of
-  // 64 keys bf16 7.5 / 5.8, 128 8.0 / 7.8, 256 8.0 / 12.3; 16 of 256 12.8 / 12.6;
-  // 64 of 256 16.3 / 14.8; e4m3 (32 keys a tile) 1 of 256 8.8 / 9.2.  16/1 heads
-  // have twice the work per tile: 16 of 64 keys 9.7 / 9.0, of 128 10.3 / 11.7.
-  const int whole_tiles = (items >= 128 ? 16 : 8) / NT;
-  p.whole = ((int64_t)p.c.table_width << p.c.page_shift) <= whole_tiles * G::KEYS ? 1 : 0;
-  if (p.whole) {
-    p.by_item = 0;
-    if (items < grid) grid = (int)items;
-  }
-  auto kern = decode_kernel<DQK, FP8, NT>;
+  // A table with room for few keys: nothing is cut, and nothing is left to join.
+  // The block's warps share a (sequence, head tile), or take one each where
+  // there are many.  Us, line / block / warp, 32/8 heads bf16, all of the table
+  // used: 1 sequence of 64 keys 7.2 / 3.5 / 5.1, 256 keys 8.1 / 5.0 / 11, 512
+  // keys 8.3 / 7.0 / 20, 1024 keys 8.7 / 11 / 36; 64 of 256 21 / 17 / 16; 256 of
+  // 64 23 / 26 / 18, of 512 96 / 89 / 85.  e4m3: 1 of 512 8.3 / 5.5, of 1024 8.8 /
+  // 8.1.  16/1 heads: 4 of 512 9.0 / 8.4.
+  p.share = ((int64_t)p.c.table_width << p.c.page_shift) > 512 ? 0 : items >= 4 * num_sms ? 1 : G::WARPS;
+  auto kern = p.share > 0 ? decode_kernel<DQK, FP8, NT, 0> : decode_kernel<DQK, FP8, NT, 1>;
+  if (p.share > 0 && items < grid) grid = (int)items;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
   if (e != cudaSuccess) return e;
   e = launch_overlapped(kern, dim3((unsigned)grid), dim3(G::THREADS), G::SMEM, st, p);
-  if (e != cudaSuccess) return e;
-  if (p.whole) return cudaSuccess;
+  if (e != cudaSuccess || p.share > 0) return e;
   if (p.by_item)
     return launch_overlapped(decode_join_kernel<1>, dim3((unsigned)items, (unsigned)rows), dim3(kItemWarps * 32), 0, st, p, entries);
   const unsigned blocks = (unsigned)((entries + kJoinWarps - 1) / kJoinWarps);

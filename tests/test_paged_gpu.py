@@ -138,14 +138,30 @@ def test_decode_splits_and_joins(dtype, lens):
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("hq,hkv,dqk,page", [(8, 2, 128, 16), (40, 2, 128, 64), (16, 16, 192, 1), (6, 3, 192, 16)])
-def test_decode_small_tables_take_a_warp_per_sequence(dtype, hq, hkv, dqk, page):
-    # at most 4 (16 heads) or 8 tiles of 16 keys: nothing is split
+def test_decode_tiny_tables(dtype, hq, hkv, dqk, page):
+    # 64 keys: some warps of a block get none
     lens = [0, 1, 15, 16, 17, 31, 33, 48, 0, 47]
     c = Cache(lens, hkv, dqk, page, dtype, seed=18)
     assert (c.table.shape[1] - (page > 1)) * page <= 64  # (the table has a column to spare)
     a = c.cuda()
     a["block_table"] = a["block_table"][:, :max(1, 64 // page)].contiguous()
     q = _q(len(lens), hq, dqk)
+    out, lse = _zq().attn_decode(q.cuda(), **a)
+    check_decode(c, q, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hkv,dqk,page,n", [(8, 2, 128, 16, 40), (8, 2, 128, 64, 300), (40, 2, 128, 64, 20), (24, 2, 192, 16, 150), (3, 3, 192, 1, 200), (16, 1, 128, 64, 600)])
+def test_decode_small_tables_are_one_launch(dtype, hq, hkv, dqk, page, n):
+    # room for 512 keys: a block for each (sequence, head tile), or a warp each from 592 of them on
+    lens = [(89 * i) % 497 if i % 7 else 0 for i in range(n - 1)] + [511 if page == 1 else 496]
+    c = Cache(lens, hkv, dqk, page, dtype, seed=28)
+    assert c.table.shape[1] * page in (512, 576)
+    a = c.cuda()
+    a["block_table"] = a["block_table"][:, :512 // page]  # (the table has a column to spare)
+    a["block_table"][3, 1] = -1
+    c.table[3, 1] = -1
+    q = _q(n, hq, dqk)
     out, lse = _zq().attn_decode(q.cuda(), **a)
     check_decode(c, q, out, lse)
 
