@@ -20,7 +20,8 @@
 //     decode_join_kernel joins the parts: M = max m_j, l = sum l_j 2^(m_j - M),
 //     o = sum O_j 2^(m_j - M) / l.  The order is fixed, so runs repeat bit for
 //     bit.  Where the table has room for few keys there is no line: the warps of
-//     a block share a (sequence, kv head) and join in shared memory.
+//     a block, or of a cluster of up to 8, share a (sequence, kv head) and join in
+//     shared memory.
 //     Pieces go to warps side by side: where the heads allow it, the 2 or 4
 //     warps of a team walk the same keys of adjacent heads, so that the 256
 //     (bf16) or 128 (e4m3) bytes that a head has of a key are read together
@@ -72,7 +73,9 @@ struct DecodeParams {
   // where by_item, else one per entry [piece][team], of the one it begins
   int4* cut;
   int by_item;
-  int share;     // without a line: warps that share a (sequence, head tile), 1 or all of the block
+  // without a line: warps that share a (sequence, head tile), 1 or all of a
+  // cluster of 2^cluster_log2 blocks
+  int share, cluster_log2;
   float* part;   // [piece][team][2][slot]: slot 0 a segment begun by an earlier piece, slot 1 one left to later pieces
 };
 
@@ -109,6 +112,30 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
+}
+
+// All blocks of the cluster; what they wrote to shared memory is visible after it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Loads from the same place of block `rank`'s shared memory.
+__device__ __forceinline__ uint32_t peer_address(const void* p, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float2 ld_cluster2(const void* p, int rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(peer_address(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(const void* p, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(peer_address(p, rank))
+               : "memory");
+  return v;
 }
 
 __device__ __forceinline__ int keys_of(const PagedKV& c, int b) {
@@ -233,20 +260,23 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
   const int flat = c.Hkv * p.head_tiles;
   // without a line: items are (sequence, flat head tile)
   const bool shared = !LINE && p.share > 1;
-  const int64_t items = (int64_t)c.B * flat;
-  int64_t item = shared ? blockIdx.x : blockIdx.x + (int64_t)warp * gridDim.x;
+  const int ranks = LINE ? 1 : 1 << p.cluster_log2, rank = blockIdx.x & (ranks - 1);
+  const unsigned items = (unsigned)c.B * flat;  // (at most 65535 * 4096)
+  unsigned item = shared ? blockIdx.x >> p.cluster_log2 : blockIdx.x + warp * gridDim.x;
   while (LINE ? x < x1 : item < items) {
-    if (!LINE) b = (int)(item / flat);
+    if (!LINE) b = (int)(item / (unsigned)flat);
     const int len = keys_of(c, b);
     const int tiles = (len + G::KEYS - 1) / G::KEYS, span = tiles + kSegmentCost;
     int fh, t0 = 0, steps = tiles;
     int64_t start = 0;
     if constexpr (!LINE) {
-      fh = (int)(item % flat);
-      item += shared ? gridDim.x : (int64_t)gridDim.x * WARPS;
-      if (shared) {  // a part of the keys each
-        t0 = tiles * warp / WARPS;
-        steps = tiles * (warp + 1) / WARPS - t0;
+      static_assert(WARPS == 4, "a shift by 2");
+      fh = (int)item - b * flat;
+      item += shared ? gridDim.x >> p.cluster_log2 : gridDim.x * WARPS;
+      if (shared) {  // a part of the keys each (few: below 2^16 tiles)
+        const int at = rank * WARPS + warp, sh = p.cluster_log2 + 2;
+        t0 = tiles * at >> sh;
+        steps = (tiles * (at + 1) >> sh) - t0;
       }
       if (len == 0) continue;
     } else {
@@ -628,9 +658,25 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
         Part all;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) all.add(stat_s[w][h], *reinterpret_cast<const float4*>(turn_of(w) + h * PITCH + lane * 4));
-        write_row(h, all.m, all.l, all.a);
+        if (ranks == 1) {
+          write_row(h, all.m, all.l, all.a);
+        } else {  // the block's part, in warp 0's place
+          __syncwarp();
+          *reinterpret_cast<float4*>(turn_of(0) + h * PITCH + lane * 4) = all.a;
+          if (lane == 0) stat_s[0][h] = make_float2(all.m, all.l);
+        }
       }
-      __syncthreads();  // (the rings are loaded again)
+      if (ranks == 1) {
+        __syncthreads();  // (the rings are loaded again)
+      } else {
+        cluster_sync();
+        for (int h = rank * WARPS + warp; h < rows; h += ranks * WARPS) {
+          Part all;
+          for (int r = 0; r < ranks; ++r) all.add(ld_cluster2(&stat_s[0][h], r), ld_cluster4(turn_of(0) + h * PITCH + lane * 4, r));
+          write_row(h, all.m, all.l, all.a);
+        }
+        cluster_sync();  // (the others have read this block's part)
+      }
     }
     if (LINE && begins) {
       // its parts: this piece's and those up to the one of its last place.
@@ -763,19 +809,37 @@ cudaError_t launch_kernel(DecodeParams& p, cudaStream_t st, int num_sms) {
   // blocks, 11.4 / 9.9 and 86 x 1000 keys, 2752 blocks, 70 / 61).
   const int rows = p.group < kMaxHeads ? p.group : kMaxHeads;
   p.by_item = items * rows <= 4 * num_sms && items <= entries ? 1 : 0;
-  // A table with room for few keys: nothing is cut, and nothing is left to join.
-  // The block's warps share a (sequence, head tile), or take one each where
-  // there are many.  Us, line / block / warp, 32/8 heads bf16, all of the table
-  // used: 1 sequence of 64 keys 7.2 / 3.5 / 5.1, 256 keys 8.1 / 5.0 / 11, 512
-  // keys 8.3 / 7.0 / 20, 1024 keys 8.7 / 11 / 36; 64 of 256 21 / 17 / 16; 256 of
-  // 64 23 / 26 / 18, of 512 96 / 89 / 85.  e4m3: 1 of 512 8.3 / 5.5, of 1024 8.8 /
-  // 8.1.  16/1 heads: 4 of 512 9.0 / 8.4.
-  p.share = ((int64_t)p.c.table_width << p.c.page_shift) > 512 ? 0 : items >= 4 * num_sms ? 1 : G::WARPS;
+  // A table with room for few keys: nothing is cut, and nothing is left to join
+  // in another launch.  A (sequence, head tile) is a cluster's of 1 to 8 blocks,
+  // as many as are resident at once and have 8 tiles of the table each, as long
+  // as a warp has no more than 8; or one warp's, where there are many and the
+  // tables short.  Us, line / that, equal lengths, 32/8 heads bf16: 1 sequence of
+  // 512 keys 7.8 / 5.2, 1024 8.6 / 5.8, 4096 11.4 / 9.2 (8192: 12.2 / 14.5, so the
+  // line); 4 of 4096 19.2 / 15.9; 16 of 1024 21.5 / 15.2, of 1 to 1024 14.2 / 9.9
+  // (4096: 52.0 / 45.6, but ragged ones are better off in the line); 64 of 512
+  // 31.7 / 27.1; 256 of 64 23.3 / 17.7 by warps, 26.1 by blocks.  e4m3: 1 of 1024
+  // 8.6 / 5.5; 16/1 heads, 64 of 2048 24.6 / 11.8, of 1 to 2048 22.5 / 11.1; 16/16
+  // heads 192/128, 64 of 1 to 1024 38.4 / 42.8 by warps, so the line.  Clusters of
+  // 1 / 2 / 4 / 8: 1 sequence bf16 of 256 keys 5.5 / 5.5 / 5.0 / 5.5, of 1024 11.8 /
+  // 8.8 / 6.8 / 6.4.
+  const int64_t tiles = (((int64_t)p.c.table_width << p.c.page_shift) + G::KEYS - 1) / G::KEYS;
+  int cluster = 1;
+  p.share = p.cluster_log2 = 0;
+  if (items >= 4 * num_sms || (items > grid && tiles <= 4)) {
+    if (tiles <= 16) p.share = 1;
+  } else {
+    while (cluster < 8 && tiles >= 16 * cluster && items * 2 * cluster <= grid) cluster *= 2;
+    if (tiles <= 32 * cluster) p.share = cluster * G::WARPS;
+  }
+  if (p.share > 0) {
+    while ((1 << p.cluster_log2) < cluster) ++p.cluster_log2;
+    if (items * cluster < grid) grid = (int)items * cluster;
+    grid -= grid % cluster;
+  }
   auto kern = p.share > 0 ? decode_kernel<DQK, FP8, NT, 0> : decode_kernel<DQK, FP8, NT, 1>;
-  if (p.share > 0 && items < grid) grid = (int)items;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_overlapped(kern, dim3((unsigned)grid), dim3(G::THREADS), G::SMEM, st, p);
+  e = launch_overlapped_cluster(kern, p.share > 0 ? (unsigned)cluster : 1u, dim3((unsigned)grid), dim3(G::THREADS), G::SMEM, st, p);
   if (e != cudaSuccess || p.share > 0) return e;
   if (p.by_item)
     return launch_overlapped(decode_join_kernel<1>, dim3((unsigned)items, (unsigned)rows), dim3(kItemWarps * 32), 0, st, p, entries);

@@ -153,7 +153,7 @@ def test_decode_tiny_tables(dtype, hq, hkv, dqk, page):
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("hq,hkv,dqk,page,n", [(8, 2, 128, 16, 40), (8, 2, 128, 64, 300), (40, 2, 128, 64, 20), (24, 2, 192, 16, 150), (3, 3, 192, 1, 200), (16, 1, 128, 64, 600)])
 def test_decode_small_tables_are_one_launch(dtype, hq, hkv, dqk, page, n):
-    # room for 512 keys: a block for each (sequence, head tile), or a warp each from 592 of them on
+    # room for 512 keys: a block or two for each (sequence, head tile), e4m3 a warp each from 592 of them on
     lens = [(89 * i) % 497 if i % 7 else 0 for i in range(n - 1)] + [511 if page == 1 else 496]
     c = Cache(lens, hkv, dqk, page, dtype, seed=28)
     assert c.table.shape[1] * page in (512, 576)
@@ -163,6 +163,31 @@ def test_decode_small_tables_are_one_launch(dtype, hq, hkv, dqk, page, n):
     c.table[3, 1] = -1
     q = _q(n, hq, dqk)
     out, lse = _zq().attn_decode(q.cuda(), **a)
+    check_decode(c, q, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hkv,dqk,room,n", [(8, 2, 128, 256, 300), (16, 1, 128, 128, 700), (12, 4, 192, 64, 90)])
+def test_decode_tables_taken_by_a_warp(dtype, hq, hkv, dqk, room, n):
+    lens = [(37 * i) % (room - 15) if i % 5 else 0 for i in range(n - 1)] + [room - 16]
+    c = Cache(lens, hkv, dqk, 16, dtype, seed=48)
+    assert c.table.shape[1] * 16 == room
+    q = _q(n, hq, dqk)
+    out, lse = _zq().attn_decode(q.cuda(), **c.cuda())
+    check_decode(c, q, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hkv,dqk,room,n", [(8, 2, 128, 256, 9), (8, 2, 128, 1024, 60), (40, 2, 128, 2048, 5), (16, 1, 192, 4096, 3),
+                                               (6, 3, 192, 2048, 12), (8, 1, 128, 4096, 37), (4, 1, 128, 8192, 2)])
+def test_decode_tables_shared_by_a_cluster(dtype, hq, hkv, dqk, room, n):
+    # 2, 4 and 8 blocks a (sequence, head tile); 4096 bf16 and 8192 e4m3 keys are the most
+    lens = [[room - 32, 0, 1, 33, room // 2 + 5, 700 % room, 129, 16][i % 8] for i in range(n)]
+    c = Cache(lens, hkv, dqk, 32, dtype, seed=38)
+    assert c.table.shape[1] * 32 == room
+    c.table[0, 2] = -1
+    q = _q(n, hq, dqk)
+    out, lse = _zq().attn_decode(q.cuda(), **c.cuda())
     check_decode(c, q, out, lse)
 
 
