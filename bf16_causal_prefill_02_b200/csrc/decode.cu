@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
         t0 = tiles * at >> sh;
         steps = (tiles * (at + 1) >> sh) - t0;
       }
-      if (len == 0) continue;
+      if (len == 0 && !shared) continue;  // (shared: the barriers below are everyone's, whatever a length does meanwhile)
     } else {
       if (len == 0 || off >= (int64_t)span * heads) {
         off -= len == 0 ? 0 : (int64_t)span * heads;
