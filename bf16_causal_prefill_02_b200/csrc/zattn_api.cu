@@ -14,7 +14,7 @@
 
 namespace {
 
-constexpr int kVersion = 100;  // 0.1.0
+constexpr int kVersion = 200;  // 0.2.0
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // bound on any single device-side wait
 constexpr int64_t kMaxGroupedSlots = 65535;      // grouped quantiser: slots are grid.y
 
