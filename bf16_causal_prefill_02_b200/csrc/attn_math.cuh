@@ -14,6 +14,7 @@
 namespace zq {
 
 constexpr int kInvalidExp = -(1 << 20);
+constexpr float kTiniest = 1.17549435e-38f;  // 2^-126, the smallest normal fp32
 
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
