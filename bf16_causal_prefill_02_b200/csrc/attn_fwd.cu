@@ -527,6 +527,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float kds = p.k_descale ? p.k_descale[di] : 1.0f;
       vscale = p.v_descale ? p.v_descale[di] : 1.0f;
       c = ((p.softmax_scale * qds) * kds) * 1.4426950408889634f;
+      // A scale of 0 (a head of zeros), or a product that vanishes: all scores
+      // are 0.  A factor that leaves them 0, and not 0 itself, which would
+      // turn the masked keys' -inf into NaN.
+      if (c == 0.0f) c = kTiniest;
     }
     for (int j = 0; ok && j < n_kv; ++j) {
       const int jg = jt + j;

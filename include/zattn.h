@@ -85,8 +85,9 @@ extern "C" {
  *   (bottom-right alignment); a query row with no visible key gets out = 0,
  *   lse = -inf.
  *   q/k/v_descale: device pointers to one fp32 each (per-tensor dequant
- *   scale, FP8 only; NULL means 1.0); ignored for bf16.  Per-(batch, kv
- *   head) descales go through zq_attn_fwd_ex (descale_layout).
+ *   scale, FP8 only; NULL means 1.0); ignored for bf16.  0 or above; 0, which
+ *   the quantiser gives a tensor of zeros, makes all scores (v: the output) 0.
+ *   Per-(batch, kv head) descales go through zq_attn_fwd_ex (descale_layout).
  *   FP8 uses Lean P with per-(row, 64-key block) power-of-2 scaling and
  *   headroom 8 (see zq_attn_fwd_ex for the other modes).
  * Errors: ZQ_ERR_NULL (q, k, v or out NULL), ZQ_ERR_SHAPE, ZQ_ERR_UNSUPPORTED,

@@ -92,3 +92,20 @@ def test_packed_prompts_quantised_with_a_head_of_zeros(mode):
     assert torch.isfinite(out).all() and torch.isfinite(lse).all()
     for h in (2, 3):
         _check_means(out[:, h].cpu(), lse[h].cpu(), (cv[0, :, 1].float() * dv[0, 1]).cpu(), 500, 500, True)
+
+
+@pytest.mark.parametrize("mode", ["exact", "leanp"])
+@pytest.mark.parametrize("dqk", [128, 192])
+@pytest.mark.parametrize("sq,sk,causal", [(200, 200, True), (130, 400, True), (300, 150, True), (77, 200, False)])
+def test_fixed_batch_with_a_zero_head(mode, dqk, sq, sk, causal):
+    zq = _zq()
+    q, k, v = _codes(2 * sq, 4, dqk, 11).view(2, sq, 4, dqk), _codes(2 * sk, 2, dqk, 12).view(2, sk, 2, dqk), _codes(2 * sk, 2, 128, 13).view(2, sk, 2, 128)
+    ds = {x: torch.full((2, 2), 0.02) for x in "qkv"}
+    ds["k"][0, 1], k[0, :, 1] = 0.0, 0.0
+    ds["q"][1, 0], ds["k"][1, 0] = 1e-30, 1e-30  # the product is 0 in 32 bits
+    out, lse = zq.attn_fwd(q.cuda(), k.cuda(), v.cuda(), causal=causal, softmax_mode=zq.ZQ_SOFTMAX_EXACT if mode == "exact" else zq.ZQ_SOFTMAX_LEANP,
+                           **{x + "_descale": ds[x].cuda() for x in ds})
+    for b, g in ((0, 1), (1, 0)):
+        for h in (2 * g, 2 * g + 1):
+            _check_means(out[b, :, h].cpu(), lse[b, h].cpu(), v[b, :, g].float() * ds["v"][b, g], sq, sk, causal)
+    assert torch.isfinite(out).all()
