@@ -12,7 +12,9 @@
 //     side by side (NT = 2), larger groups further head tiles.
 //   * P^T is rounded to bf16 twice, P = P_hi + P_lo, over a bf16 cache: the
 //     tensor work is not what bounds the kernel and the output keeps the 32-bit
-//     weights' precision.  Over an e4m3 cache P is f16.
+//     weights' precision.  Over an e4m3 cache P is f16, which is exact to 2^-11
+//     from 2^-14 on; the weights are kept near the top of its range (Weights),
+//     so that many keys far below one (an attention sink) still count.
 //   * The cache's length is split.  All key tiles of all (sequence, kv head)
 //     pairs form one line that is cut into equal pieces, one per warp, so
 //     ragged lengths cost no balance.  A piece that holds a whole (sequence,
@@ -55,6 +57,19 @@ constexpr int kJoinWarps = 4;
 constexpr int kItemWarps = 8;
 constexpr int kJoinBatch = 8;  // parts' rows on their way at once
 constexpr int kJoinAlone = 24;  // parts that one warp joins by itself
+// The reference of the weights 2^(s - ref) moves when one would pass 2^kTop, to
+// where the largest is 2^kHead.  bf16 weights have fp32's range: 2^8 and 1.
+// f16's range ends at 2^16 and its 11 bits at 2^-14, so e4m3 caches take 2^15 and
+// 2^11: weights down to 2^-25 of the largest keep their bits, and a smaller one
+// is off by 2^-36 of the largest at most.  (With 2^8 and 1 a key 25.6 octaves
+// above 10^5 others took all of their weight.  The time is the same: 128 x up to
+// 16384 keys 176.0 us with 2^8 and 1, 176.0 with 2^15 and 2^7, 176.6 with 2^15
+// and 2^11; 64 x 8192 keys 185.1, 185.5, 184.1.)
+template <int FP8>
+struct Weights {
+  static constexpr float kTop = FP8 ? 15.0f : 8.0f;
+  static constexpr float kHead = FP8 ? 11.0f : 0.0f;
+};
 constexpr unsigned kJoinStep = 733;  // prime, and no divisor of a number of entries (at most 1280)
 
 struct DecodeParams {
@@ -164,6 +179,7 @@ struct Part {
 template <int DQK, int FP8, int NT, int LINE>
 __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) decode_kernel(const DecodeParams p) {
   using G = DecGeo<DQK, FP8, NT>;
+  using W = Weights<FP8>;
   constexpr int DV = G::DV, NS = G::NS, WARPS = G::WARPS, THREADS = G::THREADS;
   constexpr unsigned kFull = 0xffffffffu;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -515,9 +531,8 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
           for (int i = 0; i < 2; ++i) {
             mx[nt][i] = fmaxf(sc[nt][0][i], sc[nt][0][2 + i]);
             if constexpr (G::KB == 2) mx[nt][i] = fmaxf(mx[nt][i], fmaxf(sc[nt][1][i], sc[nt][1][2 + i]));
-            move |= mx[nt][i] > ref[nt][i] + 8.0f;
+            move |= mx[nt][i] > ref[nt][i] + W::kTop;
           }
-        // the reference moves when a score passes it by 8 (weights stay below 2^8)
         if (__any_sync(kFull, move)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -527,7 +542,7 @@ __global__ void __launch_bounds__(DecGeo<DQK, FP8, NT>::THREADS, kCtasPerSm) dec
               m = fmaxf(m, __shfl_xor_sync(kFull, m, 4));
               m = fmaxf(m, __shfl_xor_sync(kFull, m, 8));
               m = fmaxf(m, __shfl_xor_sync(kFull, m, 16));
-              const float nref = fmaxf(ref[nt][i], m);
+              const float nref = fmaxf(ref[nt][i], m - W::kHead);
               const float f = (nref == -INFINITY || nref == ref[nt][i]) ? 1.0f : ex2_approx(ref[nt][i] - nref);
               ref[nt][i] = nref;
               l[nt][i] *= f;

@@ -480,8 +480,9 @@ ZQ_API int zq_kv_append(const zq_paged_kv* cache, const void* k, const void* v, 
  * A sequence without keys (length 0, or no key on a page of the cache) gets
  * out = 0, lse = -inf.  Rows past a sequence's length are not read.  e4m3
  * codes enter the products exactly (as f16); the weights enter as the sum of
- * two bf16 values (bf16 caches) or rounded to f16 (e4m3 caches), sums are
- * fp32.  One stream operation where the table has room for few keys, else two
+ * two bf16 values (bf16 caches) or rounded to f16 (e4m3 caches: to 2^-11 of
+ * the weight down to 2^-25 of the row's largest, below that to 2^-36 of the
+ * largest), sums are fp32.  One stream operation where the table has room for few keys, else two
  * (kernels).  Runs repeat bit for bit.
  * Errors: as zq_kv_append, with q, out, lse and workspace.
  */
