@@ -485,6 +485,9 @@ int zq_attn_decode(const zq_paged_kv* cache, const void* q, int64_t q_stride, in
   if (!std::isfinite(softmax_scale)) return ZQ_ERR_SHAPE;
   const int64_t qr = (int64_t)Hq * cache->d_qk, qs = q_stride ? q_stride : qr;
   if (qs < qr || qs > ((int64_t)1 << 31)) return ZQ_ERR_SHAPE;
+  // The line of key tiles (at most a 16th of the keys of all heads, and 5 a
+  // sequence and head) times its pieces (at most 1280) stays in 63 bits.
+  if ((int64_t)cache->B * Hq > ((int64_t)1 << 53) / ((int64_t)cache->table_width * cache->page_size)) return ZQ_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || (lse && !aligned16(lse)) || qs % 8 != 0)
     return ZQ_ERR_ALIGN;
   int sms = 0;

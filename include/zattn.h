@@ -484,7 +484,8 @@ ZQ_API int zq_kv_append(const zq_paged_kv* cache, const void* k, const void* v, 
  * the weight down to 2^-25 of the row's largest, below that to 2^-36 of the
  * largest), sums are fp32.  One stream operation where the table has room for few keys, else two
  * (kernels).  Runs repeat bit for bit.
- * Errors: as zq_kv_append, with q, out, lse and workspace.
+ * Errors: as zq_kv_append, with q, out, lse and workspace; ZQ_ERR_SHAPE also
+ *   for B * Hq * table_width * page_size past 2^53.
  */
 ZQ_API int zq_attn_decode(const zq_paged_kv* cache, const void* q, int64_t q_stride, int Hq,
                           float softmax_scale, void* out, float* lse, void* workspace, void* stream);
