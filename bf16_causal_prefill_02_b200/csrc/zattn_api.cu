@@ -19,6 +19,7 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;  // bound on any single device-si
 constexpr int64_t kMaxGroupedSlots = 65535;      // grouped quantiser: slots are grid.y
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Current device must be sm_100 (B200 class).  Returns the SM count through
 // `num_sms` when non-null.
@@ -94,7 +95,7 @@ const char* zq_status_string(int s) {
     case ZQ_ERR_NULL: return "a required pointer is NULL";
     case ZQ_ERR_SHAPE: return "invalid shape (size <= 0, Hq % Hkv != 0 or too large)";
     case ZQ_ERR_UNSUPPORTED: return "unsupported head dims, dtype, mode or option";
-    case ZQ_ERR_ALIGN: return "pointer not 16-byte aligned";
+    case ZQ_ERR_ALIGN: return "pointer not aligned (16 bytes; 4 for tables, lengths, offsets and scales)";
     case ZQ_ERR_ARCH: return "current device is not sm_100 (B200)";
     case ZQ_ERR_CUDA: return "CUDA call failed";
     case ZQ_ERR_TIMEOUT: return "a device-side wait timed out";
@@ -372,6 +373,8 @@ int zq_attn_varlen_fwd(const zq_varlen_args* a, void* stream) {
   const int64_t max_tiles = zq::varlen_tiles(a->total_q, a->B, zq::kTile);
   if (max_tiles * a->Hq > 0x7FFF0000ll) return ZQ_ERR_SHAPE;
   if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->out) || !aligned16(a->lse)) return ZQ_ERR_ALIGN;
+  if (!aligned4(a->cu_seqlens_q) || !aligned4(a->cu_seqlens_k) || !aligned4(a->status)) return ZQ_ERR_ALIGN;
+  if (a->dtype == ZQ_DTYPE_FP8_E4M3 && (!aligned4(a->q_descale) || !aligned4(a->k_descale) || !aligned4(a->v_descale))) return ZQ_ERR_ALIGN;
   int sms = 0;
   rc = check_device(&sms);
   if (rc != ZQ_OK) return rc;
@@ -428,6 +431,8 @@ static int paged_cache(const zq_paged_kv* a, zq::PagedKV* c) {
   const int64_t ks = a->k_page_stride ? a->k_page_stride : kp, vs = a->v_page_stride ? a->v_page_stride : vp;
   if (ks < kp || vs < vp || ks > ((int64_t)1 << 40) || vs > ((int64_t)1 << 40)) return ZQ_ERR_SHAPE;
   if (!aligned16(a->k_cache) || !aligned16(a->v_cache) || (ks * es) % 16 != 0 || (vs * es) % 16 != 0) return ZQ_ERR_ALIGN;
+  if (!aligned4(a->block_table) || !aligned4(a->cache_seqlens)) return ZQ_ERR_ALIGN;
+  if (a->dtype == ZQ_DTYPE_FP8_E4M3 && (!aligned4(a->k_descale) || !aligned4(a->v_descale))) return ZQ_ERR_ALIGN;
   c->k = static_cast<char*>(a->k_cache);
   c->v = static_cast<char*>(a->v_cache);
   c->k_page = ks * es;
@@ -460,7 +465,7 @@ int zq_kv_append(const zq_paged_kv* cache, const void* k, const void* v, int64_t
   const int64_t kr = (int64_t)cache->Hkv * cache->d_qk, vr = (int64_t)cache->Hkv * cache->d_v;
   const int64_t ks = k_stride ? k_stride : kr, vs = v_stride ? v_stride : vr;
   if (ks < kr || vs < vr || ks > ((int64_t)1 << 31) || vs > ((int64_t)1 << 31)) return ZQ_ERR_SHAPE;
-  if (!aligned16(k) || !aligned16(v) || ks % 8 != 0 || vs % 8 != 0) return ZQ_ERR_ALIGN;
+  if (!aligned16(k) || !aligned16(v) || !aligned4(cu_seqlens) || ks % 8 != 0 || vs % 8 != 0) return ZQ_ERR_ALIGN;
   rc = check_device(nullptr);
   if (rc != ZQ_OK) return rc;
   L.k = static_cast<const char*>(k);

@@ -61,7 +61,7 @@ extern "C" {
 #define ZQ_ERR_NULL (-1)        /* a required pointer is NULL              */
 #define ZQ_ERR_SHAPE (-2)       /* a size <= 0, Hq % Hkv != 0, overflow    */
 #define ZQ_ERR_UNSUPPORTED (-3) /* head dims, dtype, mode or option        */
-#define ZQ_ERR_ALIGN (-4)       /* a pointer is not 16-byte aligned        */
+#define ZQ_ERR_ALIGN (-4)       /* a pointer or stride is not aligned      */
 #define ZQ_ERR_ARCH (-5)        /* current device is not sm_100            */
 #define ZQ_ERR_CUDA (-6)        /* a CUDA driver/runtime call failed       */
 #define ZQ_ERR_TIMEOUT (-7)     /* a device-side wait ran out (status word) */
@@ -368,7 +368,8 @@ ZQ_API size_t zq_quantize_grouped_workspace_bytes(int B, int H, int heads_per_sc
  * infinity is NaN); what other rows hold does not matter.
  * total_q == 0 does nothing; total_k == 0 gives 0 and -inf (k, v may be NULL).
  * One kernel launch, no workspace.  Errors: as zq_attn_fwd_ex; ZQ_ERR_SHAPE
- * also for B > 65535, Hq > 4096 and (total_q / 128 + B) * Hq past 31 bits.
+ * also for B > 65535, Hq > 4096 and (total_q / 128 + B) * Hq past 31 bits;
+ * ZQ_ERR_ALIGN also for offsets, status and descales not 4-byte aligned.
  */
 typedef struct zq_varlen_args {
   const void* q;
@@ -459,7 +460,8 @@ typedef struct zq_paged_kv {
  *   cu_seqlens, a stride too small, page_size no power of two, products past
  *   the limits above), ZQ_ERR_UNSUPPORTED (head dims, dtype, descale_per_head
  *   not 0 or 1), ZQ_ERR_ALIGN (k, v, caches or strides not multiples of 16
- *   bytes), ZQ_ERR_ARCH, ZQ_ERR_CUDA.
+ *   bytes; table, lengths, offsets or descales not of 4), ZQ_ERR_ARCH,
+ *   ZQ_ERR_CUDA.
  */
 ZQ_API int zq_kv_append(const zq_paged_kv* cache, const void* k, const void* v, int64_t k_stride,
                         int64_t v_stride, const int32_t* cu_seqlens, int64_t T, void* stream);
