@@ -715,6 +715,8 @@ def kv_append(k, v, k_cache, v_cache, block_table, cache_seqlens, cu_seqlens=Non
     bfloat16, or FP8 e4m3 with fp32 descales (one value, or one per kv head):
     written in place.  Sequence b's tokens go to positions cache_seqlens[b]
     onwards of the pages in block_table[b]; cache_seqlens is not advanced.
+    Tokens of a sequence whose length is below 0 (a slot of a padded batch),
+    or whose place lies past the table or on no page, are dropped.
     Returns (k_cache, v_cache)."""
     torch = _torch()
     c, device, B, Hkv, dqk, dv = _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale)
@@ -742,7 +744,7 @@ def attn_decode(q, k_cache, v_cache, block_table, cache_seqlens, out=None, lse=N
     """Attention of one new token per sequence over a paged cache, as zq_attn_decode.
 
     q (B,Hq,d_qk) bfloat16 (rows may be strided); the cache as for kv_append,
-    with cache_seqlens (int32, B) keys in each sequence.
+    with cache_seqlens (int32, B) keys in each sequence (below 0: none).
     Returns (out bf16 (B,Hq,d_v), lse fp32 (B,Hq) or None)."""
     torch = _torch()
     c, device, B, Hkv, dqk, dv = _paged_kv(k_cache, v_cache, block_table, cache_seqlens, k_descale, v_descale)

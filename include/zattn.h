@@ -411,7 +411,9 @@ ZQ_API int zq_attn_varlen_fwd(const zq_varlen_args* args, void* stream);
  *   block_table  (B, >= table_width) int32, table_stride entries from one
  *            sequence to the next (0 means table_width)
  *   cache_seqlens  B int32: keys the cache holds for each sequence.  A value
- *            below 0 counts as 0, one above table_width * page_size as that.
+ *            above table_width * page_size counts as that.  One below 0 (a
+ *            slot of a padded batch) stands for no keys and takes none:
+ *            zq_attn_decode counts it as 0, zq_kv_append drops the tokens.
  *   page_size a power of two up to 65536; (d_qk, d_v) in {(128,128), (192,128)};
  *   table_width * page_size at most 2^30, B at most 65535, heads at most 4096.
  *   k_descale, v_descale: e4m3 only.  The value of a code is code * descale.
@@ -449,9 +451,9 @@ typedef struct zq_paged_kv {
  *   cu_seqlens[b].  bf16 caches take the bits as they are; e4m3 caches
  *   e4m3_rne_satfinite(fl32(x * fl32(1 / descale))), and code 0 where the
  *   descale is 0 and x is finite.
- * cache_seqlens is read, not advanced.  Tokens of no sequence, and tokens
- * whose position lies past the table or on a page outside [0, num_pages), are
- * dropped.  Two tokens that the table sends to the same place are the
+ * cache_seqlens is read, not advanced.  Tokens of no sequence, those of a
+ * sequence whose length is below 0, and those whose position lies past the
+ * table or on a page outside [0, num_pages), are dropped.  Two tokens that the table sends to the same place are the
  * caller's error: that place then holds parts of either.  Offsets that do not
  * ascend leave open which sequence a token goes to, or whether it is dropped;
  * nothing outside the cache's pages is written.
