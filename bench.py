@@ -234,21 +234,30 @@ def cpu_model() -> str:
 
 def kernel_sources_digest(read=None) -> str:
     """sha256 over the attention kernels' sources: attn_fwd.cu, attn_pp.cu
-    and every header beside them, by name in sorted order.  `read(name)`
-    returns a file's bytes (default: the files in csrc)."""
+    and the headers beside them that these include, also through one another,
+    by name in sorted order.  `read(name)` returns a file's bytes, read(None)
+    the names (default: the files in csrc)."""
     import hashlib
+    import re
 
     csrc = os.path.join(ROOT, "bf16_causal_prefill_02_b200", "csrc")
     if read is None:
-        names = sorted(n for n in os.listdir(csrc) if n in ("attn_fwd.cu", "attn_pp.cu") or n.endswith((".h", ".cuh")))
-
         def read(n):
+            if n is None:
+                return os.listdir(csrc)
             with open(os.path.join(csrc, n), "rb") as f:
                 return f.read()
-    else:
-        names = sorted(read(None))
+    there = set(read(None))
+    names, todo = set(), [n for n in ("attn_fwd.cu", "attn_pp.cu") if n in there]
+    while todo:
+        n = todo.pop()
+        if n in names:
+            continue
+        names.add(n)
+        included = re.findall(rb'^[ \t]*#[ \t]*include[ \t]*"([^"]+)"', read(n), re.M)
+        todo += [i.decode() for i in included if i.decode() in there]
     h = hashlib.sha256()
-    for n in names:
+    for n in sorted(names):
         h.update(n.encode() + b"\0" + read(n) + b"\0")
     return h.hexdigest()
 

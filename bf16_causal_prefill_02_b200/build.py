@@ -21,7 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libzattn.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["zattn_api.cu", "quantize.cu", "attn_fwd.cu", "attn_pp.cu", "attn_varlen.cu", "attn_varlen_pp.cu", "kv_append.cu", "decode.cu"]
-HEADERS = ["sm100_ptx.cuh", "zq_internal.h", "schedule.h", "attn_math.cuh", "paged.cuh", "varlen_sched.cuh"]
+HEADERS = ["sm100_ptx.cuh", "zq_internal.h", "schedule.h", "serving.h", "attn_math.cuh", "paged.cuh", "varlen_sched.cuh"]
 
 
 def nvcc() -> str:

@@ -35,10 +35,9 @@
 #include <type_traits>
 
 #include "attn_math.cuh"
-#include "schedule.h"
+#include "serving.h"
 #include "sm100_ptx.cuh"
 #include "varlen_sched.cuh"
-#include "zq_internal.h"
 
 namespace zq {
 

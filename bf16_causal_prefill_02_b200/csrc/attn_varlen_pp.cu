@@ -8,7 +8,7 @@
 // team's softmax runs while the tensor core works for the other.
 //
 // The tiles are two consecutive ones of one head; the earlier stops at its own
-// diagonal.  Which calls come here: use_varlen_pairs (schedule.h).
+// diagonal.  Which calls come here: use_varlen_pairs (serving.h).
 //
 // Bound by the softmax chain and, in longer runs, by the board's power: 32/8
 // heads after a pause, 16384 rows 1679 us (1310 TFLOP/s), 12 prompts of 13.6K
@@ -25,10 +25,9 @@
 #include <type_traits>
 
 #include "attn_math.cuh"
-#include "schedule.h"
+#include "serving.h"
 #include "sm100_ptx.cuh"
 #include "varlen_sched.cuh"
-#include "zq_internal.h"
 
 namespace zq {
 

@@ -5,8 +5,8 @@
 #include <cstdint>
 
 #include "attn_math.cuh"
+#include "serving.h"
 #include "sm100_ptx.cuh"
-#include "zq_internal.h"
 
 namespace zq {
 

@@ -115,34 +115,6 @@ inline int choose_head_group(int B, int Hq, int Hkv, int Sq, int Sk, int d_qk, i
   return bh;
 }
 
-// Packed prompts: a bound on the query tiles of `rows` rows, which the host
-// knows without the offsets.
-inline int varlen_tiles(int64_t Tq, int64_t B, int rows) {
-  return Tq > 0 ? (int)((Tq + (rows - 1) * B) / rows) : 0;
-}
-
-// Packed prompts, BF16 at d = 128: two tiles per CTA (attn_varlen_pp.cu) where
-// there are enough units to keep the SMs even, and sequences long enough to
-// fill both tiles.  Measured against one tile per CTA (us, one / two):
-//   units of 256 rows  192: 29.8 / 31.9   376: 252 / 257   416: 87 / 90
-//   472: 44.4 / 46.7   512: 237 / 232     640: 197 / 190   1024: 469 / 449
-//   41 sequences of 100 rows, 32 heads: 34.5 / 43.5.
-inline bool use_varlen_pairs(int64_t Tq, int64_t B, int Hq, int num_sms) {
-  return 3 * (int64_t)varlen_tiles(Tq, B, 2 * kTile) * Hq >= 10 * (int64_t)num_sms && Tq >= 2 * kTile * B;
-}
-
-// Packed prompts: heads whose units are interleaved.  All of them, which
-// balances best, while the K and V of all heads are below 256 MB; else the
-// query heads of as many kv heads as stay below.  (All heads against 4 at a
-// time: 32/8 heads, 4096 rows bf16 137 against 163 us, FP8 112 against 151;
-// MLA, 16 heads, 16384 rows and 168 MB of K and V 1418 against 1498 us.)
-inline int choose_varlen_head_group(int Hq, int Hkv, int64_t Tk, int d_qk, int d_v, int elem_bytes) {
-  const double one = (double)Tk * (d_qk + d_v) * elem_bytes;
-  int kv = Hkv;
-  while (kv > 1 && (Hkv % kv != 0 || kv * one > 256.0 * 1024 * 1024)) --kv;
-  return Hq / Hkv * kv;
-}
-
 // Short sequences (at most 64 query tiles) run persistent: one CTA per SM,
 // each walking its share of the units, so that a unit's loads and first QK
 // overlap the previous unit's tail.  Longer ones launch a CTA per unit: the

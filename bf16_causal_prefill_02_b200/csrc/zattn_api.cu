@@ -10,6 +10,7 @@
 #include "zattn.h"
 
 #include "schedule.h"
+#include "serving.h"
 #include "zq_internal.h"
 
 namespace {

@@ -87,101 +87,6 @@ struct QuantItems {
 cudaError_t launch_quantize_multi(QuantItems Q, int count, void* workspace, cudaStream_t st, int num_sms);
 void* noalloc_scratch_for_device(int dev);
 
-// A launch whose blocks may become resident while the stream's previous kernel
-// still runs.  The kernel calls griddepcontrol.wait before it touches memory,
-// which returns once that kernel's writes are visible; nothing else changes in
-// the stream's order.
-template <class... P, class... A>
-inline cudaError_t launch_overlapped_cluster(void (*kern)(P...), unsigned cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                                             const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, P(args)...);
-}
-template <class... P, class... A>
-inline cudaError_t launch_overlapped(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A&... args) {
-  return launch_overlapped_cluster(kern, 1, grid, block, smem, st, args...);
-}
-
-// Attention over packed prompts.
-struct VarlenParams {
-  void* out;   // (Tq, Hq, d_v) bfloat16
-  float* lse;  // (Hq, Tq) or nullptr
-  const int32_t* cu_q;  // B + 1 row offsets
-  const int32_t* cu_k;
-  const float* q_descale;
-  const float* k_descale;
-  const float* v_descale;
-  int* status;
-  int descale_per_kv;  // entry b * Hkv + kv head, as in AttnParams
-  int B, Tq, Tk, Hq, Hkv, group;
-  int max_tiles;   // bound on the 128-row query tiles of all sequences
-  int head_group;  // query heads whose units are interleaved; divides Hq
-  int causal;
-  int headroom_T;
-  float scale_log2;  // softmax scale times log2(e)
-  uint64_t timeout_ns;
-};
-struct VarlenLaunch {
-  const void* q;
-  const void* k;
-  const void* v;
-  VarlenParams p;
-  int dqk, dtype, mode, block_scale;
-  bool pairs;  // two query tiles per CTA (BF16, d = 128)
-};
-cudaError_t launch_attention_varlen(const VarlenLaunch& a, cudaStream_t st);
-cudaError_t launch_attention_varlen_pp(const VarlenLaunch& a, cudaStream_t st);
-
-// A paged cache as the kernels address it: key c of sequence b is row
-// c & (page_size - 1) of page block_table[b * table_stride + (c >> page_shift)].
-// Strides in bytes.
-struct PagedKV {
-  char* k;
-  char* v;
-  int64_t k_page, v_page;
-  const int32_t* table;
-  const int32_t* seqlens;
-  const float* k_descale;  // 1 or Hkv fp32, or nullptr (1.0)
-  const float* v_descale;
-  int64_t table_stride;
-  int descale_per_head;
-  int B, Hkv, num_pages, page_shift, table_width;
-  int dqk, dv, dtype;
-};
-struct AppendLaunch {
-  PagedKV c;
-  const char* k;
-  const char* v;
-  int64_t k_stride, v_stride;  // bytes between tokens
-  const int32_t* cu;           // B + 1 token offsets, or nullptr (token t is sequence t's)
-  int64_t T;
-  int shares;  // warps per token (set by the launcher)
-};
-cudaError_t launch_kv_append(const AppendLaunch& a, cudaStream_t st);
-struct DecodeLaunch {
-  PagedKV c;
-  const void* q;
-  int64_t q_stride;  // elements between sequences
-  int Hq;
-  float scale_log2;
-  void* out;
-  float* lse;
-  void* workspace;
-};
-cudaError_t launch_decode(const DecodeLaunch& a, cudaStream_t st, int num_sms);
-size_t decode_workspace_bytes();
 cudaError_t launch_exp2_check(const float* x, float* y, int64_t n, int degree, cudaStream_t st);
 size_t noalloc_scratch_capacity();
 
