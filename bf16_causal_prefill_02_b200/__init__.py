@@ -129,6 +129,8 @@ def _load():
     lib.zq_quantize_noalloc_scratch_bytes.restype = ctypes.c_size_t
     lib.zq_attn_varlen_fwd.argtypes = [ctypes.POINTER(zq_varlen_args), P]
     lib.zq_attn_varlen_fwd.restype = i32
+    lib.zq_attn_varlen_debug.argtypes = [ctypes.POINTER(zq_varlen_args), i32, P]
+    lib.zq_attn_varlen_debug.restype = i32
     lib.zq_kv_append.argtypes = [ctypes.POINTER(zq_paged_kv), P, P, i64, i64, P, i64, P]
     lib.zq_kv_append.restype = i32
     lib.zq_attn_decode.argtypes = [ctypes.POINTER(zq_paged_kv), P, i64, i32, f32, P, P, P, P]
@@ -241,6 +243,10 @@ def zq_quantize_noalloc_scratch_bytes() -> int:
 
 def zq_attn_varlen_fwd(args: zq_varlen_args, stream) -> int:
     return _lib.zq_attn_varlen_fwd(ctypes.byref(args), stream)
+
+
+def zq_attn_varlen_debug(args: zq_varlen_args, flags, stream) -> int:
+    return _lib.zq_attn_varlen_debug(ctypes.byref(args), flags, stream)
 
 
 def zq_kv_append(cache: zq_paged_kv, k, v, k_stride, v_stride, cu_seqlens, T, stream) -> int:
@@ -595,7 +601,7 @@ def _row_stride(name, t):
 
 def attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, out=None, lse=None, softmax_scale=None, causal=True, q_descale=None,
                 k_descale=None, v_descale=None, softmax_mode=ZQ_SOFTMAX_LEANP, block_scale=True, headroom_T=8, status=None,
-                return_lse=True, stream=None):
+                return_lse=True, stream=None, debug_flags=0):
     """Causal prefill attention over packed prompts, as zq_attn_varlen_fwd.
 
     q (total_q,Hq,d_qk), k (total_k,Hkv,d_qk), v (total_k,Hkv,d_v): bfloat16,
@@ -652,7 +658,10 @@ def attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, out=None, lse=None, softmax
         a = zq_varlen_args(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(e), cu_seqlens_q.data_ptr(),
                            cu_seqlens_k.data_ptr(), B, Tq, Tk, Hq, Hkv, dqk, dv, scale, 1 if causal else 0, dtype, qd, kd, vd,
                            int(softmax_mode), 1 if block_scale else 0, int(headroom_T), _ptr(status), layout)
-        _check(zq_attn_varlen_fwd(a, s), "zq_attn_varlen_fwd")
+        if debug_flags:
+            _check(zq_attn_varlen_debug(a, int(debug_flags), s), "zq_attn_varlen_debug")
+        else:
+            _check(zq_attn_varlen_fwd(a, s), "zq_attn_varlen_fwd")
         return o, e
 
     return _on(device, stream, call)

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kVarThreads, 1)
     for (int s = 0; s < 4 * NS; ++s) mbar_init(bars + s, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar_sfull + s, 1);
-      mbar_init(bar_pfull + s, kSmThreads);
+      mbar_init(bar_pfull + s, kSmThreads + p.withhold);
       mbar_init(bar_ufull + s, 1);
       mbar_init(bar_ufree + s, 2 + kSmThreads / 32);  // producer, issuer, softmax warps
     }

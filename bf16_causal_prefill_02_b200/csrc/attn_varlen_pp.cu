@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(kVppThreads, 1)
       mbar_init(bar_qfree + t, 1);
       mbar_init(bar_sfull + t, 1);
       mbar_init(bar_sfree + t, kTeam);
-      mbar_init(bar_pfull + 2 * t, kTeam);
-      mbar_init(bar_pfull + 2 * t + 1, kTeam);
+      mbar_init(bar_pfull + 2 * t, kTeam + p.withhold);
+      mbar_init(bar_pfull + 2 * t + 1, kTeam + p.withhold);
       mbar_init(bar_pvdone + t, 1);
       mbar_init(bar_ofinal + t, 1);
       mbar_init(bar_ofree + t, kTeam);

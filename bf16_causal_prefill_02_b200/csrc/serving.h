@@ -55,6 +55,10 @@ struct VarlenParams {
   int headroom_T;
   float scale_log2;  // softmax scale times log2(e)
   uint64_t timeout_ns;
+  // Test hook, else 0: arrivals that the barriers of P expect and nobody makes,
+  // so that the issuers wait for P until their limit and all others for them.
+  // (A test in the issuers' loops cost the two-tile kernel 1 to 2%.)
+  int withhold;
 };
 struct VarlenLaunch {
   const void* q;

@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kVersion = 200;  // 0.2.0
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // bound on any single device-side wait
+constexpr uint64_t kDebugTimeoutNs = 100000000ull;  // the same in a packed call that is made to give up
 constexpr int64_t kMaxGroupedSlots = 65535;      // grouped quantiser: slots are grid.y
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -361,7 +362,7 @@ int zq_quantize_fp8_grouped(const void* x, int x_dtype, int B, int64_t S, int H,
   return e == cudaSuccess ? ZQ_OK : ZQ_ERR_CUDA;
 }
 
-int zq_attn_varlen_fwd(const zq_varlen_args* a, void* stream) {
+static int varlen_impl(const zq_varlen_args* a, int flags, void* stream) {
   if (!a) return ZQ_ERR_NULL;
   if (!a->cu_seqlens_q || !a->cu_seqlens_k) return ZQ_ERR_NULL;
   if (a->B <= 0 || a->B > 65535 || a->total_q < 0 || a->total_k < 0 || a->Hq <= 0 || a->Hkv <= 0 || a->Hq > 4096)
@@ -411,9 +412,17 @@ int zq_attn_varlen_fwd(const zq_varlen_args* a, void* stream) {
   p.causal = a->causal ? 1 : 0;
   p.headroom_T = fp8 ? a->headroom_T : 8;
   p.scale_log2 = scale_log2(a->softmax_scale, a->d_qk);
-  p.timeout_ns = kTimeoutNs;
+  p.timeout_ns = flags ? kDebugTimeoutNs : kTimeoutNs;
+  p.withhold = flags;
   cudaError_t e = zq::launch_attention_varlen(L, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ZQ_OK : ZQ_ERR_CUDA;
+}
+
+int zq_attn_varlen_fwd(const zq_varlen_args* a, void* stream) { return varlen_impl(a, 0, stream); }
+
+int zq_attn_varlen_debug(const zq_varlen_args* a, int flags, void* stream) {
+  if (flags & ~1) return ZQ_ERR_UNSUPPORTED;
+  return varlen_impl(a, flags, stream);
 }
 
 // The cache as the kernels address it, after validation.

@@ -395,6 +395,14 @@ typedef struct zq_varlen_args {
 
 ZQ_API int zq_attn_varlen_fwd(const zq_varlen_args* args, void* stream);
 
+/* zq_attn_varlen_debug -- zq_attn_varlen_fwd made to give up.  flags: 0 (as
+ * zq_attn_varlen_fwd), or 1: the MMA issuers never learn that P is written, so
+ * that every bounded wait, here 0.1 s, runs out while loads and products are on
+ * their way: the kernel writes ZQ_ERR_TIMEOUT to args->status and returns (some
+ * tenths of a second later) with the outputs undefined; nothing faults or
+ * hangs.  For tests. */
+ZQ_API int zq_attn_varlen_debug(const zq_varlen_args* args, int flags, void* stream);
+
 /*
  * A paged key-value cache.  Pages hold page_size keys of every kv head; key c
  * of sequence b is row c % page_size of page block_table[b * table_stride +

@@ -35,3 +35,12 @@ def test_offsets_of_tokens_must_be_aligned():
 @pytest.mark.parametrize("kw", ["cu_seqlens_q", "cu_seqlens_k", "status", "q_descale", "k_descale", "v_descale"])
 def test_words_of_a_pack_must_be_aligned(kw):
     assert zq.zq_attn_varlen_fwd(_varlen(dtype=1, **{kw: A + 2}), None) == zq.ZQ_ERR_ALIGN
+
+
+@pytest.mark.parametrize("flags", [2, -1, 1 << 30])
+def test_unknown_debug_flags_are_refused(flags):
+    assert zq.zq_attn_varlen_debug(_varlen(), flags, None) == zq.ZQ_ERR_UNSUPPORTED
+
+
+def test_debug_entry_checks_its_arguments():
+    assert zq.zq_attn_varlen_debug(_varlen(q=None), 1, None) == zq.ZQ_ERR_NULL
