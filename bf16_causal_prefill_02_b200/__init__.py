@@ -608,6 +608,7 @@ def attn_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, out=None, lse=None, softmax
     or FP8 e4m3 with fp32 descales (one value each, or B * Hkv values, one per
     sequence and kv head).  cu_seqlens_q, cu_seqlens_k: int32 CUDA tensors of
     B + 1 ascending row offsets.
+    debug_flags is for tests (zq_attn_varlen_debug).
     Returns (out bf16 (total_q,Hq,d_v), lse fp32 (Hq,total_q) or None); rows
     of no sequence are not written."""
     torch = _torch()
