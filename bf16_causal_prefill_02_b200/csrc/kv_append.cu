@@ -47,10 +47,12 @@ __device__ __forceinline__ uint2 to_e4m3(uint4 x, float inv) {
   return make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
 }
 
-// A scale of 0 stands for a head whose values were all 0: its codes are 0.
+// A scale of 0 stands for a head whose values were all 0: its codes are 0.  The
+// reciprocal of a scale below 2^-128 passes fp32's range; it is cut there, so
+// that a value of 0 does not become NaN.
 __device__ __forceinline__ float inverse_scale(const float* ds, int per_head, int h) {
   const float s = ds ? ds[per_head ? h : 0] : 1.0f;
-  return s == 0.0f ? 0.0f : __frcp_rn(s);
+  return s == 0.0f ? 0.0f : fminf(__frcp_rn(s), 3.40282347e+38f);
 }
 
 // Pieces of a key and of a value row that a lane has on their way before it

@@ -457,8 +457,8 @@ typedef struct zq_paged_kv {
  *      sequence (T must equal B).
  *   Token t of sequence b goes to position cache_seqlens[b] + t -
  *   cu_seqlens[b].  bf16 caches take the bits as they are; e4m3 caches
- *   e4m3_rne_satfinite(fl32(x * fl32(1 / descale))), and code 0 where the
- *   descale is 0 and x is finite.
+ *   e4m3_rne_satfinite(fl32(x * fl32(1 / descale))), the reciprocal at most
+ *   the largest fp32, and code 0 where the descale is 0 and x is finite.
  * cache_seqlens is read, not advanced.  Tokens of no sequence, those of a
  * sequence whose length is below 0, and those whose position lies past the
  * table or on a page outside [0, num_pages), are dropped.  Two tokens that the table sends to the same place are the
